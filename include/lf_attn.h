@@ -191,6 +191,133 @@ lf_status lf_attn_merge_rows(const float* ml, const float* acc, int n_parts, int
                              const int32_t* out_pos, void* out, int T_out, lf_dtype dtype, void* stream);
 
 /*
+ * Rotary positions in front of the attention, and behind its backward pass.
+ *
+ * lf_attn_rotary -- turns q and k by their positions and copies v beside
+ * them, from rows of any strides (a packed projection, say) to rows of any
+ * strides (the contiguous [B, H, T, d] of lf_attn_fwd, say), asynchronous on
+ * `stream`.  Pair i of a row's first `rot` values, (x, y), becomes
+ *   a (x cos t - y sin t),  a (y cos t + x sin t),   t = position * freqs[i],
+ * with a = amplitude; the pairs are (i, i + rot/2), or (2i, 2i + 1) when
+ * `interleaved`.  The values behind rot are copied.  `inverse` turns by -t:
+ * the transpose, which takes gradients of the turned rows to gradients of
+ * the rows (the fp32 dq, dk, dv of lf_attn_bwd back to a packed projection).
+ * Angles are formed in 64 bits, the products in 32, rounded once.
+ *
+ *   q, k, v, q_out, k_out, v_out   DEVICE; each of q, k, v may be NULL
+ *               together with its output, not all three
+ *   strides     HOST int64 [18]: (sample, head, token) strides in elements of
+ *               q, k, v, q_out, k_out, v_out; the d values of a row are
+ *               contiguous.  Strides of inputs may be 0, those of outputs
+ *               not; no output may overlap an input.
+ *   B, T, q_heads, kv_heads   sizes; B and T may be 0
+ *   d           1..256;  rot: even, 0..d (0: a copy; freqs may be NULL)
+ *   pos         DEVICE int32, [T] per sample at a stride of pos_stride (0:
+ *               shared by all); NULL: 0 .. T-1
+ *   freqs       DEVICE double [rot / 2], radians per position
+ *   in_dtype, out_dtype   the same, or LF_F32 to a 16-bit type
+ *   Pointers are aligned to their element.  16-byte aligned rows with
+ *   d % 16 == 0 and rot % 16 == 0 (8 when interleaved) move 16 values at a
+ *   time; others go value by value.
+ */
+lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
+                         const int64_t* strides, int B, int q_heads, int kv_heads, int T, int d, const int32_t* pos,
+                         int64_t pos_stride, const double* freqs, int rot, int interleaved, int inverse,
+                         float amplitude, lf_dtype in_dtype, lf_dtype out_dtype, void* stream);
+
+/*
+ * The paged cache: the same attention for models that answer token by token.
+ *
+ * A token at position p of its sequence attends, on kv head h, to
+ *   N(p) = { p - dil[h] * t : 0 <= t <= r, p - dil[h] * t >= 0 }
+ *          U { g in G : g <= p }                         for p not in G;
+ *   N(p) = 0 .. p                                        for p in G,
+ * each key once: the forward's key set with nothing behind the token, so the
+ * last row of lf_attn_fwd over the same keys is the same row.  q_heads /
+ * kv_heads query heads share a kv head.
+ *
+ * The cache has n_pages pages of `page` tokens (a power of two, 8..256);
+ * table DEVICE int32 [n_seqs, max_pages] names the page that holds positions
+ * [i * page, (i + 1) * page) of a sequence, and entries that no token reaches
+ * are not read.  A page may be in several tables (a shared prefix) as long as
+ * no call appends to it for two of them.
+ *   bits 16: k_cache, v_cache [n_pages, kv_heads, page, d] in `dtype`.
+ *   bits 4:  k_cache, v_cache [n_pages, kv_heads, page, d / 2] bytes of codes
+ *            and k_par, v_par [n_pages, kv_heads, page, d / 32, 2] fp16: each
+ *            group of 32 values is mid + scale (c - 8), c = 0..15, par =
+ *            (scale, mid).  With n = d / 32, a K row is 32-bit words [4][n],
+ *            word [c][g] holding values 32 g + 8 c + 0..7 from its lowest
+ *            four bits up; a V row is 16-bit units [8][n], unit [r][g]
+ *            holding values 32 g + 4 r + 0..3.
+ * dtype is LF_BF16 or LF_F16 (queries, output, dense rows), d is 64 or 128,
+ * q_heads <= 128 a multiple of kv_heads, n_pages * kv_heads * page < 2^31,
+ * max_pages * page <= 2^30.  Cache and par pointers are 16-byte aligned.
+ *
+ * No call below allocates or keeps anything: the plan and the workspace are
+ * the caller's, so calls with different ones may overlap on any streams, and
+ * all of them may be captured (after a first call on the device).
+ *
+ * lf_attn_cache_plan -- lays out one step on the device; every layer of the
+ * step with the same heads and window reads it.
+ *   cu_tokens   DEVICE int32 [n_seqs + 1], from 0 and not decreasing: rows
+ *               [cu[s], cu[s+1]) of the step's n_tokens token rows are
+ *               sequence s's new tokens.  Rows from cu[n_seqs] on are no
+ *               tokens: every call leaves their outputs as they were.
+ *   context     DEVICE int32 [n_seqs]: tokens of the sequence before these,
+ *               so row cu[s] + i is at position context[s] + i
+ *   global_idx  DEVICE int32 [n_seqs, n_global], any order, duplicates
+ *               allowed, n_global <= 1024; NULL iff n_global == 0.  Entries
+ *               outside [0, max_pages * page) are ignored and flagged.
+ *   r, dil      as lf_attn_fwd, dil HOST int32 [kv_heads] or NULL; an r past
+ *               the sequence is plain causal attention
+ *   plan        DEVICE, lf_attn_cache_plan_bytes(n_seqs, n_tokens, n_global)
+ *               bytes (0 for invalid sizes), 256-byte aligned
+ *
+ * lf_attn_cache_append -- puts the step's keys and values into the cache, the
+ * keys turned as by lf_attn_rotary at the rows' positions.
+ *   k, v        DEVICE rows [n_tokens][kv_heads][d]; q [n_tokens][q_heads][d]
+ *               or NULL: queries to turn into q_out
+ *   k_held, v_held   DEVICE dense rows for what the cache now holds (the
+ *               dequantised values for bits 4), or NULL
+ *   strides     HOST int64 [12]: (token, head) strides in elements of k, v,
+ *               q, k_held, v_held, q_out (those of NULL rows are not read);
+ *               no output may overlap an input
+ *   rot == 0    leaves keys and queries as they are
+ *   4 bits: scale = fp16((max - min) / 15), mid = fp16(min + 8 scale), c =
+ *   (x - mid) / scale + 8 rounded to the nearest, ties to even (8 where scale
+ *   is 0), x being the turned value in `dtype`.  Scale and mid have fp16's
+ *   range; a group with an infinity or a NaN is held as NaN.
+ *
+ * lf_attn_cache_fwd -- the attention of the step's rows over the cache, which
+ * already holds their own keys.  q and out: DEVICE rows
+ * [n_tokens][q_heads][d], strides HOST int64 [4]: (token, head) of q, of out;
+ * q's rows are 16-byte aligned.  workspace: DEVICE,
+ * lf_attn_cache_workspace_bytes(q_heads, kv_heads, d) bytes, 16-byte aligned,
+ * of this call alone while it runs.  The plan must have been made with the
+ * same n_seqs, n_tokens, n_global, page, max_pages, heads, r and dil
+ * (lf_attn_cache_append: n_seqs, n_tokens, page and max_pages); a call with
+ * another plan computes nothing and flags it.
+ *
+ * A row at a position outside its table, and a key on a page outside
+ * [0, n_pages), are left out and flagged (lf_attn_device_status).
+ */
+uint64_t lf_attn_cache_plan_bytes(int n_seqs, int n_tokens, int n_global);
+lf_status lf_attn_cache_plan(const int32_t* cu_tokens, const int32_t* context, int n_seqs, int n_tokens,
+                             const int32_t* global_idx, int n_global, int page, int max_pages, int q_heads,
+                             int kv_heads, int r, const int32_t* dil, void* plan, void* stream);
+lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void* k_held, void* v_held, void* q_out,
+                               const int64_t* strides, void* k_cache, void* v_cache, void* k_par, void* v_par,
+                               int n_pages, int page, const int32_t* table, int max_pages, const void* plan, int n_seqs,
+                               int n_tokens, int n_global, int q_heads, int kv_heads, int d, const double* freqs,
+                               int rot, int interleaved, float amplitude, lf_dtype dtype, int bits, void* stream);
+uint64_t lf_attn_cache_workspace_bytes(int q_heads, int kv_heads, int d);
+lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, const void* k_cache, const void* v_cache,
+                            const void* k_par, const void* v_par, int n_pages, int page, const int32_t* table,
+                            int max_pages, const void* plan, int n_seqs, int n_tokens, int n_global, int q_heads,
+                            int kv_heads, int d, int r, const int32_t* dil, float scale, lf_dtype dtype, int bits,
+                            void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
  * lf_attn_fwd_stages -- runs a subset of the kernels lf_attn_fwd queues, for
  * timing one kernel at a time.  Same arguments as lf_attn_fwd, plus
  * stage_mask: bit 0 = prep (global lists, padding, packed global keys),
@@ -213,6 +340,9 @@ lf_status lf_attn_fwd_stages(const void* q, const void* k, const void* v, void* 
  * (may be NULL) receives the raw bits:
  *   bit 0  global_idx entry out of range (ignored by the computation)
  *   bit 1  a pipeline wait timed out; that call's output is incomplete
+ *   bit 2  paged cache: a row or a key outside its table or the pages, or
+ *          cu_tokens not as described (left out of the computation)
+ *   bit 3  paged cache: a plan made for other sizes; nothing was computed
  */
 lf_status lf_attn_device_status(void* stream, uint32_t* flags);
 

@@ -1,0 +1,280 @@
+// kv_plan.cuh -- the plan of one step over the paged cache: which sequence
+// and position each token row has, the sorted global tokens of each sequence,
+// and how the attention's work is split over its CTAs.  Made on the device
+// from device data (so a captured step replans itself on every replay) and
+// read by all layers of the step with the same heads and window.
+//
+// The work sequence: token rows in order; per row its units, one per kv head
+// and group of at most 16 query heads of it; per unit its 64-key blocks, the
+// window's first, then those of the sequence's global list.  CTA s of G takes
+// blocks [s W / G', (s + 1) W / G') of all W, G' = min(G, W), so every CTA has the same number
+// of blocks, give or take one, however ragged the lengths are.  A unit that a
+// range boundary cuts leaves a partial state in every CTA that has a piece of
+// it, and one CTA of the merge kernel joins them.
+//
+// Bound: latency (a few KB).  The global lists take one CTA per sequence; the
+// rows, their prefix sum and the split one CTA in all, since each needs the
+// whole of the one before.
+#pragma once
+#include "lf_common.cuh"
+#include "ptx.cuh"
+
+namespace lf {
+
+constexpr int kKvBlock = 64;           // keys per block of the work sequence
+constexpr int kKvMaxGlobal = 1024;     // global tokens per sequence (the lists are ranked in O(n^2))
+constexpr int kKvMaxCtas = 2048;
+constexpr int kPlanThreads = 1024;
+constexpr uint32_t kStatusBadCache = 4u;  // a row or page of a cache call outside its range (left out)
+constexpr uint32_t kStatusBadPlan = 8u;   // a cache call with another plan than its arguments say
+
+struct KvCut {
+    int32_t row, unit;  // the unit that CTA s begins and a later one ends
+    int32_t last;       // its last CTA; -1: CTA s begins no such unit
+    int32_t pad;
+};
+struct KvStart {
+    int32_t row, unit, blk, pad;
+};
+
+struct KvPlan {  // views into the caller's plan buffer
+    uint64_t* sig;       // [2]: of the rows (append), of rows and work (attention)
+    int64_t* total;      // W
+    int64_t* prefix;     // [N + 1] blocks before each row
+    KvStart* start;      // [G]
+    KvCut* cut;          // [G]
+    int32_t* row_seq;    // [N], -1: the row is none (behind the last sequence, or out of range)
+    int32_t* row_pos;    // [N]
+    int32_t* row_ng;     // [N] entries of the global list below the row's position; -1: a global row (all keys)
+    int32_t* g_count;    // [S]
+    int32_t* g_list;     // [S][n_global] sorted, each once
+};
+
+struct KvShape {  // what a plan is made for
+    int S, N, n_global, max_len;
+    int q_heads, kv_heads, nsub, r, G;
+    uint64_t sig_rows, sig_all;
+    int32_t dil[kMaxHeads];
+};
+
+// Places in the plan buffer (bytes, 256-byte aligned).
+struct KvPlanLayout {
+    size_t prefix, start, cut, seq, pos, ng, gcount, glist, total;
+};
+inline KvPlanLayout kv_plan_layout(int S, int N, int n_global) {
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    KvPlanLayout L;
+    L.prefix = 256;
+    L.start = up(L.prefix + sizeof(int64_t) * (size_t(N) + 1));
+    L.cut = up(L.start + sizeof(KvStart) * kKvMaxCtas);
+    L.seq = up(L.cut + sizeof(KvCut) * kKvMaxCtas);
+    L.pos = up(L.seq + sizeof(int32_t) * size_t(N));
+    L.ng = up(L.pos + sizeof(int32_t) * size_t(N));
+    L.gcount = up(L.ng + sizeof(int32_t) * size_t(N));
+    L.glist = up(L.gcount + sizeof(int32_t) * size_t(S));
+    L.total = up(L.glist + sizeof(int32_t) * size_t(S) * n_global);
+    return L;
+}
+inline KvPlan kv_plan_view(void* buf, const KvPlanLayout& L) {
+    uint8_t* b = static_cast<uint8_t*>(buf);
+    KvPlan p;
+    p.sig = reinterpret_cast<uint64_t*>(b);
+    p.total = reinterpret_cast<int64_t*>(b + 16);
+    p.prefix = reinterpret_cast<int64_t*>(b + L.prefix);
+    p.start = reinterpret_cast<KvStart*>(b + L.start);
+    p.cut = reinterpret_cast<KvCut*>(b + L.cut);
+    p.row_seq = reinterpret_cast<int32_t*>(b + L.seq);
+    p.row_pos = reinterpret_cast<int32_t*>(b + L.pos);
+    p.row_ng = reinterpret_cast<int32_t*>(b + L.ng);
+    p.g_count = reinterpret_cast<int32_t*>(b + L.gcount);
+    p.g_list = reinterpret_cast<int32_t*>(b + L.glist);
+    return p;
+}
+
+// A unit's keys.  Window key n of n_win sits at position first + n * step; the
+// blocks of the global list follow (entries inside the window are left out
+// there, so each key counts once).
+struct KvKeys {
+    int first, step, n_win, blocks_win, ng;
+    __host__ __device__ KvKeys(int pos, int ng_row, int r, int dil) {
+        step = ng_row < 0 ? 1 : dil;
+        const int back = ng_row < 0 ? pos : (pos / dil < r ? pos / dil : r);
+        n_win = back + 1;
+        first = pos - back * step;
+        blocks_win = (n_win + kKvBlock - 1) / kKvBlock;
+        ng = ng_row < 0 ? 0 : ng_row;
+    }
+    __host__ __device__ int blocks() const { return blocks_win + (ng + kKvBlock - 1) / kKvBlock; }
+};
+
+// Sorts a sequence's global tokens, each once.  grid: S; smem: 2 n_global ints.
+__global__ void __launch_bounds__(256) kv_plan_globals_kernel(const int32_t* gidx, int n_global, int max_len, KvPlan p,
+                                                              uint32_t* status) {
+    extern __shared__ int32_t s_g[];
+    int32_t* s_keep = s_g + n_global;
+    const int s = blockIdx.x;
+    for (int i = threadIdx.x; i < n_global; i += 256) {
+        const int g = gidx[int64_t(s) * n_global + i];
+        s_g[i] = g;
+        if (g < 0 || g >= max_len) atomicOr(status, kStatusBadGlobal);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_global; i += 256) {
+        const int g = s_g[i];
+        bool keep = g >= 0 && g < max_len;
+        for (int j = 0; j < i && keep; ++j) keep = s_g[j] != g;
+        s_keep[i] = keep;
+    }
+    __syncthreads();
+    int kept = 0;
+    for (int i = threadIdx.x; i < n_global; i += 256) {
+        if (!s_keep[i]) continue;
+        ++kept;
+        int rank = 0;
+        for (int j = 0; j < n_global; ++j) rank += s_keep[j] && s_g[j] < s_g[i];
+        p.g_list[int64_t(s) * n_global + rank] = s_g[i];
+    }
+    // the last entry's rank + 1 is the count
+    __shared__ int s_n;
+    if (threadIdx.x == 0) s_n = 0;
+    __syncthreads();
+    if (kept) atomicAdd(&s_n, kept);
+    __syncthreads();
+    if (threadIdx.x == 0) p.g_count[s] = s_n;
+}
+
+// Rows, prefix sum and split.  One CTA.
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_t* cu, const int32_t* context,
+                                                                    const __grid_constant__ KvShape sh, KvPlan p,
+                                                                    uint32_t* status) {
+    __shared__ int64_t s_warp[32];
+    __shared__ int64_t s_carry;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s_carry = 0;
+    for (int s = tid; s <= sh.S; s += kPlanThreads) {
+        const int c = cu[s];
+        if (s == 0 ? c != 0 : c < cu[s - 1]) atomicOr(status, kStatusBadCache);
+        if (s == sh.S && c > sh.N) atomicOr(status, kStatusBadCache);
+    }
+    for (int n0 = 0; n0 < sh.N; n0 += kPlanThreads) {
+        const int n = n0 + tid;
+        int64_t blocks = 0;
+        if (n < sh.N) {
+            int lo = 0, hi = sh.S;  // the last s with cu[s] <= n
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cu[mid] <= n) lo = mid;
+                else hi = mid;
+            }
+            const int c0 = cu[lo], c1 = cu[lo + 1];
+            int seq = -1, pos = 0, ng = 0;
+            if (c0 >= 0 && c0 <= n && n < c1) {
+                const int64_t at = int64_t(context[lo]) + (n - c0);
+                if (context[lo] >= 0 && at < sh.max_len) {
+                    seq = lo;
+                    pos = static_cast<int>(at);
+                } else {
+                    atomicOr(status, kStatusBadCache);
+                }
+            }
+            if (seq >= 0) {
+                if (sh.n_global > 0) {
+                    const int32_t* g = p.g_list + int64_t(seq) * sh.n_global;
+                    const int cnt = p.g_count[seq];
+                    int a = 0, b = cnt;  // the first entry >= pos
+                    while (a < b) {
+                        const int mid = (a + b) >> 1;
+                        if (g[mid] < pos) a = mid + 1;
+                        else b = mid;
+                    }
+                    ng = (a < cnt && g[a] == pos) ? -1 : a;
+                }
+                for (int h = 0; h < sh.kv_heads; ++h) blocks += KvKeys(pos, ng, sh.r, sh.dil[h]).blocks();
+                blocks *= sh.nsub;
+            }
+            p.row_seq[n] = seq;
+            p.row_pos[n] = pos;
+            p.row_ng[n] = ng;
+        }
+        int64_t sum = blocks;  // inclusive scan over the CTA
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t t = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += t;
+        }
+        if (lane == 31) s_warp[warp] = sum;
+        __syncthreads();
+        if (warp == 0) {
+            int64_t w = s_warp[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t t = __shfl_up_sync(~0u, w, o);
+                if (lane >= o) w += t;
+            }
+            s_warp[lane] = w;
+        }
+        __syncthreads();
+        const int64_t before = s_carry + (warp ? s_warp[warp - 1] : 0) + sum - blocks;
+        if (n < sh.N) p.prefix[n] = before;
+        __syncthreads();
+        if (tid == kPlanThreads - 1) s_carry = before + blocks;
+        __syncthreads();
+    }
+    const int64_t W = s_carry;
+    if (tid == 0) {
+        p.prefix[sh.N] = W;
+        p.total[0] = W;
+        p.sig[0] = sh.sig_rows;
+        p.sig[1] = sh.sig_all;
+    }
+    __syncthreads();
+    // The split.  Block x of the sequence: its row, unit, and place in the unit.
+    const int64_t G = W < sh.G ? W : sh.G;  // no CTA below G is without a block
+    auto locate = [&](int64_t x, KvStart& at, int64_t& unit_first, int64_t& unit_end) {
+        int lo = 0, hi = sh.N;  // the last row with prefix <= x (rows without blocks are passed over)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.prefix[mid] <= x) lo = mid;
+            else hi = mid;
+        }
+        int64_t left = x - p.prefix[lo];
+        const int pos = p.row_pos[lo], ng = p.row_ng[lo];
+        int unit = 0, nb = 1;
+        for (int h = 0; h < sh.kv_heads; ++h) {
+            nb = KvKeys(pos, ng, sh.r, sh.dil[h]).blocks();
+            const int64_t all = int64_t(nb) * sh.nsub;
+            if (left < all) {
+                unit = h * sh.nsub + static_cast<int>(left / nb);
+                left %= nb;
+                break;
+            }
+            left -= all;
+        }
+        at.row = lo;
+        at.unit = unit;
+        at.blk = static_cast<int>(left);
+        at.pad = 0;
+        unit_first = x - left;
+        unit_end = unit_first + nb;
+    };
+    for (int s = tid; s < sh.G; s += kPlanThreads) {
+        const int64_t x0 = s < G ? s * W / G : 0, x1 = s < G ? (s + 1) * W / G : 0;
+        KvStart at{0, 0, 0, 0};
+        KvCut cut{0, 0, -1, 0};
+        int64_t first, end;
+        if (x0 < x1) {
+            locate(x0, at, first, end);
+            KvStart last;
+            locate(x1 - 1, last, first, end);
+            if (first >= x0 && end > x1) {
+                cut.row = last.row;
+                cut.unit = last.unit;
+                cut.last = static_cast<int>((end * G - 1) / W);  // the CTA that has block end - 1
+            }
+        }
+        p.start[s] = at;
+        p.cut[s] = cut;
+    }
+}
+
+}  // namespace lf

@@ -21,6 +21,7 @@
 #include "bwd.cuh"
 #include "global_rows.cuh"
 #include "lf_common.cuh"
+#include "lf_host.h"
 #include "prep.cuh"
 
 namespace {
@@ -660,6 +661,19 @@ lf_status static_state(StaticState** out) {
 }
 
 }  // namespace
+
+lf_status lf::device_info(cudaStream_t stream, uint32_t** status, int* sm_count) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return LF_ERR_CUDA;
+    if (!g_dev[dev].init && is_capturing(stream)) return LF_ERR_NO_MEMORY;
+    DeviceState* ds = nullptr;
+    const lf_status st = device_state(&ds);
+    if (st != LF_OK) return st;
+    *status = ds->status;
+    *sm_count = ds->sm_count;
+    return LF_OK;
+}
 
 extern "C" {
 

@@ -1,0 +1,401 @@
+// lf_cache.cu -- host side of the rotary positions and of the paged cache:
+// argument checks and launches.  No workspace is kept here: plan and partial
+// states live in buffers of the caller, so calls on different streams only
+// share the device's status word.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "lf_attn.h"
+#include "kv_append.cuh"
+#include "kv_attn.cuh"
+#include "kv_plan.cuh"
+#include "lf_common.cuh"
+#include "lf_host.h"
+#include "rotary.cuh"
+
+namespace {
+
+using namespace lf;
+
+constexpr double kLog2e = 1.4426950408889634;
+// The attention's CTAs: four per SM of a 148-SM B200 (larger GPUs run it on
+// as many), so plan and workspace have sizes known without a device.
+constexpr int kKvGrid = 148 * kKvCtasPerSm;
+static_assert(kKvGrid <= kKvMaxCtas, "");
+constexpr int kMaxRotHeads = 1024;
+constexpr int kAppendSmem = 100 * 1024;
+constexpr int kAppendTileSmem = 40 * 1024;  // staged rows of a tile of more than one token
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t size_of(lf_dtype t) { return t == LF_F32 ? 4 : 2; }
+bool known(lf_dtype t) { return t == LF_F32 || t == LF_BF16 || t == LF_F16; }
+
+// The bytes that a strided tensor reaches over.
+struct Span {
+    uintptr_t lo = 0, hi = 0;
+    bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Sizes n[i] with strides s[i] (elements) and d contiguous values behind.
+// False: a negative stride, or a place past 2^46 bytes.
+bool span_of(const void* p, int dims, const int64_t* n, const int64_t* s, int d, size_t es, Span* out) {
+    uint64_t last = 0;
+    for (int i = 0; i < dims; ++i) {
+        if (s[i] < 0) return false;
+        if (n[i] <= 1 || s[i] == 0) continue;
+        if (uint64_t(s[i]) > (uint64_t(1) << 44) / uint64_t(n[i])) return false;
+        last += uint64_t(n[i] - 1) * uint64_t(s[i]);
+    }
+    if (last > (uint64_t(1) << 44)) return false;
+    out->lo = reinterpret_cast<uintptr_t>(p);
+    out->hi = out->lo + (last + uint64_t(d)) * es;
+    return true;
+}
+
+// Rows that are written must not lie on one another: no stride of 0 over more than one.
+bool distinct(int dims, const int64_t* n, const int64_t* s) {
+    for (int i = 0; i < dims; ++i)
+        if (n[i] > 1 && s[i] == 0) return false;
+    return true;
+}
+
+bool by_eight(const void* p, int dims, const int64_t* s, size_t es) {
+    if (!aligned(p, 16)) return false;
+    for (int i = 0; i < dims; ++i)
+        if ((s[i] * int64_t(es)) % 16 != 0) return false;
+    return true;
+}
+
+// Tokens per CTA: about kRotItems items, but no fewer CTAs than two per SM.
+int tile_for(int64_t tokens, int items_per_token) {
+    const int64_t spread = (tokens + 295) / 296;
+    return static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>({int64_t(kRotMaxTile), int64_t(kRotItems) / std::max(1, items_per_token), spread})));
+}
+
+template <typename Tin, typename Tout>
+void launch_rotary(const RotaryParams& p, bool vec, dim3 grid, size_t smem, cudaStream_t s) {
+    if (vec) rotary_kernel<Tin, Tout, true><<<grid, kRotThreads, smem, s>>>(p);
+    else rotary_kernel<Tin, Tout, false><<<grid, kRotThreads, smem, s>>>(p);
+}
+
+uint64_t mix(uint64_t h, uint64_t x) {  // FNV-1a over the value's bytes
+    for (int i = 0; i < 8; ++i) h = (h ^ ((x >> (8 * i)) & 255)) * 1099511628211ull;
+    return h;
+}
+
+lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_heads, int kv_heads, int r,
+                   const int32_t* dil, KvShape* sh) {
+    if (S < 1 || N < 0 || n_global < 0 || page < 1 || max_pages < 1 || q_heads < 1 || kv_heads < 1 || r < 0)
+        return LF_ERR_INVALID_ARG;
+    if (q_heads % kv_heads != 0) return LF_ERR_INVALID_ARG;
+    if (dil)
+        for (int h = 0; h < kv_heads && h < kMaxHeads; ++h)
+            if (dil[h] < 1) return LF_ERR_INVALID_ARG;
+    if (page < 8 || page > 256 || (page & (page - 1)) != 0) return LF_ERR_UNSUPPORTED;
+    if (q_heads > kMaxHeads || n_global > kKvMaxGlobal || S > (1 << 20) || N > (1 << 20)) return LF_ERR_UNSUPPORTED;
+    if (int64_t(max_pages) * page > (int64_t(1) << 30)) return LF_ERR_UNSUPPORTED;
+    if (int64_t(S) * std::max(n_global, max_pages) > (int64_t(1) << 40)) return LF_ERR_UNSUPPORTED;
+    std::memset(sh, 0, sizeof(*sh));
+    sh->S = S;
+    sh->N = N;
+    sh->n_global = n_global;
+    sh->max_len = max_pages * page;
+    sh->q_heads = q_heads;
+    sh->kv_heads = kv_heads;
+    const int group = q_heads / kv_heads;
+    sh->nsub = (group + 15) / 16;
+    sh->r = std::min(r, sh->max_len);
+    for (int h = 0; h < kv_heads; ++h) sh->dil[h] = dil ? std::min(dil[h], sh->max_len) : 1;
+    // no more CTAs than blocks that ordinary rows can have
+    const int64_t keys = std::min<int64_t>(int64_t(sh->r) + 1, sh->max_len);
+    const int64_t blocks = (keys + kKvBlock - 1) / kKvBlock + (n_global + kKvBlock - 1) / kKvBlock;
+    sh->G = static_cast<int>(
+        std::max<int64_t>(1, std::min<int64_t>(kKvGrid, blocks * std::min(N, kKvGrid) * kv_heads * sh->nsub)));
+    uint64_t h = 14695981039346656037ull;
+    for (int64_t x : {int64_t(S), int64_t(N), int64_t(page), int64_t(max_pages)}) h = mix(h, uint64_t(x));
+    sh->sig_rows = h;
+    for (int64_t x : {int64_t(n_global), int64_t(q_heads), int64_t(kv_heads), int64_t(sh->r)}) h = mix(h, uint64_t(x));
+    for (int a = 0; a < kv_heads; ++a) h = mix(h, uint64_t(sh->dil[a]));
+    sh->sig_all = h;
+    return LF_OK;
+}
+
+int log2_of(int x) {
+    int n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
+}
+
+lf_status check_cache(const void* k, const void* v, const void* k_par, const void* v_par, int n_pages, int kv_heads,
+                      int page, int d, lf_dtype dtype, int bits) {
+    if (!k || !v || n_pages < 1 || d < 1) return LF_ERR_INVALID_ARG;
+    if (bits != 16 && bits != 4) return LF_ERR_INVALID_ARG;
+    if ((bits == 4) != (k_par != nullptr) || (bits == 4) != (v_par != nullptr)) return LF_ERR_INVALID_ARG;
+    for (const void* p : {k, v, k_par, v_par})
+        if (!aligned(p, 16)) return LF_ERR_INVALID_ARG;
+    if (!known(dtype)) return LF_ERR_INVALID_ARG;
+    if (dtype == LF_F32 || (d != 64 && d != 128)) return LF_ERR_UNSUPPORTED;
+    if (int64_t(n_pages) * kv_heads * page > INT32_MAX) return LF_ERR_UNSUPPORTED;
+    return LF_OK;
+}
+
+using AttnKernel = void (*)(KvAttnParams);
+
+template <int HD, int kBits>
+AttnKernel attn_kernel(bool half, bool two) {
+    if (half) return two ? kv_attn_kernel<HD, kBits, true, 2> : kv_attn_kernel<HD, kBits, true, 1>;
+    return two ? kv_attn_kernel<HD, kBits, false, 2> : kv_attn_kernel<HD, kBits, false, 1>;
+}
+
+}  // namespace
+
+extern "C" {
+
+lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
+                         const int64_t* strides, int B, int q_heads, int kv_heads, int T, int d, const int32_t* pos,
+                         int64_t pos_stride, const double* freqs, int rot, int interleaved, int inverse,
+                         float amplitude, lf_dtype in_dtype, lf_dtype out_dtype, void* stream) {
+    const void* x[3] = {q, k, v};
+    void* y[3] = {q_out, k_out, v_out};
+    if (!strides || B < 0 || T < 0 || q_heads < 0 || kv_heads < 0 || d < 1 || rot < 0 || rot > d || (rot & 1) ||
+        pos_stride < 0 || !std::isfinite(amplitude) || !known(in_dtype) || !known(out_dtype))
+        return LF_ERR_INVALID_ARG;
+    if ((rot > 0 && !freqs) || !aligned(freqs, 8) || !aligned(pos, 4)) return LF_ERR_INVALID_ARG;
+    if (!q && !k && !v) return LF_ERR_INVALID_ARG;
+    const size_t ei = size_of(in_dtype), eo = size_of(out_dtype);
+    RotaryParams p{};
+    Span in[3], out[3];
+    bool vec = d % 16 == 0 && (interleaved ? rot % 8 == 0 : rot % 16 == 0);
+    for (int a = 0; a < 3; ++a) {
+        if ((x[a] == nullptr) != (y[a] == nullptr)) return LF_ERR_INVALID_ARG;
+        p.heads[a] = x[a] ? (a == 0 ? q_heads : kv_heads) : 0;
+        if (!x[a]) continue;
+        if (!aligned(x[a], ei) || !aligned(y[a], eo)) return LF_ERR_INVALID_ARG;
+        const int64_t n[3] = {B, p.heads[a], T};
+        const int64_t* xs = strides + 3 * a;
+        const int64_t* ys = strides + 9 + 3 * a;
+        if (!span_of(x[a], 3, n, xs, d, ei, &in[a]) || !span_of(y[a], 3, n, ys, d, eo, &out[a]) || !distinct(3, n, ys))
+            return LF_ERR_INVALID_ARG;
+        vec = vec && by_eight(x[a], 3, xs, ei) && by_eight(y[a], 3, ys, eo);
+        p.x[a] = x[a];
+        p.y[a] = y[a];
+        std::copy(xs, xs + 3, p.xs[a]);
+        std::copy(ys, ys + 3, p.ys[a]);
+    }
+    for (const Span& a : in)
+        for (const Span& b : out)
+            if (a.meets(b)) return LF_ERR_INVALID_ARG;
+    if (in_dtype != out_dtype && in_dtype != LF_F32) return LF_ERR_UNSUPPORTED;
+    if (d > kRotMaxD || q_heads > kMaxRotHeads || kv_heads > kMaxRotHeads || B > 65535) return LF_ERR_UNSUPPORTED;
+    const int heads = p.heads[0] + p.heads[1] + p.heads[2];
+    if (B == 0 || T == 0 || heads == 0) return LF_OK;
+    p.pos = pos;
+    p.pos_stride = pos_stride;
+    p.freqs = freqs;
+    p.B = B;
+    p.T = T;
+    p.d = d;
+    p.rot = rot;
+    p.inter = interleaved ? 1 : 0;
+    p.back = inverse ? 1 : 0;
+    p.amp = amplitude;
+    p.tile = tile_for(int64_t(B) * T, heads * (vec ? d / 16 : d));
+    const dim3 grid((T + p.tile - 1) / p.tile, B);
+    const size_t smem = size_t(p.tile) * (rot / 2) * sizeof(float2);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (in_dtype == LF_F32 && out_dtype == LF_F32) launch_rotary<float, float>(p, vec, grid, smem, s);
+    else if (in_dtype == LF_F32 && out_dtype == LF_BF16) launch_rotary<float, __nv_bfloat16>(p, vec, grid, smem, s);
+    else if (in_dtype == LF_F32) launch_rotary<float, __half>(p, vec, grid, smem, s);
+    else if (in_dtype == LF_BF16) launch_rotary<__nv_bfloat16, __nv_bfloat16>(p, vec, grid, smem, s);
+    else launch_rotary<__half, __half>(p, vec, grid, smem, s);
+    return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+}
+
+uint64_t lf_attn_cache_plan_bytes(int n_seqs, int n_tokens, int n_global) {
+    if (n_seqs < 1 || n_tokens < 0 || n_global < 0 || n_seqs > (1 << 20) || n_tokens > (1 << 20) ||
+        n_global > kKvMaxGlobal)
+        return 0;
+    return kv_plan_layout(n_seqs, n_tokens, n_global).total;
+}
+
+lf_status lf_attn_cache_plan(const int32_t* cu_tokens, const int32_t* context, int n_seqs, int n_tokens,
+                             const int32_t* global_idx, int n_global, int page, int max_pages, int q_heads,
+                             int kv_heads, int r, const int32_t* dil, void* plan, void* stream) {
+    if (!cu_tokens || !context || !plan || (n_global > 0) != (global_idx != nullptr)) return LF_ERR_INVALID_ARG;
+    if (!aligned(cu_tokens, 4) || !aligned(context, 4) || !aligned(global_idx, 4) || !aligned(plan, 256))
+        return LF_ERR_INVALID_ARG;
+    KvShape sh;
+    lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, r, dil, &sh);
+    if (st != LF_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint32_t* status = nullptr;
+    int sms = 0;
+    if ((st = device_info(s, &status, &sms)) != LF_OK) return st;
+    const KvPlan p = kv_plan_view(plan, kv_plan_layout(n_seqs, n_tokens, n_global));
+    if (n_global > 0)
+        kv_plan_globals_kernel<<<n_seqs, 256, 2 * sizeof(int32_t) * n_global, s>>>(global_idx, n_global, sh.max_len, p,
+                                                                                 status);
+    kv_plan_rows_kernel<<<1, kPlanThreads, 0, s>>>(cu_tokens, context, sh, p, status);
+    return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+}
+
+lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void* k_held, void* v_held, void* q_out,
+                               const int64_t* strides, void* k_cache, void* v_cache, void* k_par, void* v_par,
+                               int n_pages, int page, const int32_t* table, int max_pages, const void* plan, int n_seqs,
+                               int n_tokens, int n_global, int q_heads, int kv_heads, int d, const double* freqs,
+                               int rot, int interleaved, float amplitude, lf_dtype dtype, int bits, void* stream) {
+    if (!k || !v || !strides || !table || !plan || (q != nullptr) != (q_out != nullptr)) return LF_ERR_INVALID_ARG;
+    if (rot < 0 || rot > d || (rot & 1) || (rot > 0 && !freqs) || !aligned(freqs, 8) || !aligned(table, 4) ||
+        !aligned(plan, 256) || !std::isfinite(amplitude))
+        return LF_ERR_INVALID_ARG;
+    KvShape sh;
+    lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, 0, nullptr, &sh);
+    if (st != LF_OK) return st;
+    if ((st = check_cache(k_cache, v_cache, k_par, v_par, n_pages, kv_heads, page, d, dtype, bits)) != LF_OK) return st;
+    KvAppendParams p{};
+    const void* x[3] = {k, v, q};
+    void* y[3] = {k_held, v_held, q_out};
+    Span in[3], out[3];
+    bool vec = interleaved ? rot % 8 == 0 : rot % 16 == 0;
+    for (int a = 0; a < 3; ++a) {
+        p.heads[a] = a < 2 ? kv_heads : (q ? q_heads : 0);
+        const int64_t n[2] = {n_tokens, p.heads[a]};
+        const int64_t* xs = strides + 2 * a;
+        const int64_t* ys = strides + 6 + 2 * a;
+        if (x[a]) {
+            if (!aligned(x[a], 2) || !span_of(x[a], 2, n, xs, d, 2, &in[a])) return LF_ERR_INVALID_ARG;
+            vec = vec && by_eight(x[a], 2, xs, 2);
+        }
+        if (y[a]) {
+            if (!aligned(y[a], 2) || !span_of(y[a], 2, n, ys, d, 2, &out[a]) || !distinct(2, n, ys))
+                return LF_ERR_INVALID_ARG;
+            vec = vec && by_eight(y[a], 2, ys, 2);
+        }
+        p.x[a] = x[a];
+        p.y[a] = y[a];
+        std::copy(xs, xs + 2, p.xs[a]);
+        std::copy(ys, ys + 2, p.ys[a]);
+    }
+    for (const Span& a : in)
+        for (const Span& b : out)
+            if (a.meets(b)) return LF_ERR_INVALID_ARG;
+    if (n_tokens == 0) return LF_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int sms = 0;
+    if ((st = device_info(s, &p.status, &sms)) != LF_OK) return st;
+    p.cache[0] = static_cast<uint8_t*>(k_cache);
+    p.cache[1] = static_cast<uint8_t*>(v_cache);
+    p.par[0] = static_cast<uint8_t*>(k_par);
+    p.par[1] = static_cast<uint8_t*>(v_par);
+    p.table = table;
+    p.plan = kv_plan_view(const_cast<void*>(plan), kv_plan_layout(n_seqs, n_tokens, n_global));
+    p.freqs = freqs;
+    p.N = n_tokens;
+    p.d = d;
+    p.rot = rot;
+    p.n_pages = n_pages;
+    p.log_page = log2_of(page);
+    p.max_pages = max_pages;
+    p.inter = interleaved ? 1 : 0;
+    p.amp = amplitude;
+    p.sig = sh.sig_rows;
+    p.tile = tile_for(n_tokens, (2 * kv_heads + p.heads[2]) * (vec ? d / 16 : d));
+    const size_t staged = bits == 4 ? size_t(2) * kv_heads * d * 2 : 0;  // per token
+    while (p.tile > 1 && staged * p.tile > size_t(kAppendTileSmem)) --p.tile;
+    const size_t smem = ((size_t(p.tile) * (rot / 2) * sizeof(float2) + 15) & ~size_t(15)) + staged * p.tile;
+    const unsigned grid = (n_tokens + p.tile - 1) / p.tile;
+    void (*kern)(KvAppendParams);
+    if (dtype == LF_F16)
+        kern = bits == 16 ? (vec ? kv_append_kernel<__half, 16, true> : kv_append_kernel<__half, 16, false>)
+                          : (vec ? kv_append_kernel<__half, 4, true> : kv_append_kernel<__half, 4, false>);
+    else
+        kern = bits == 16 ? (vec ? kv_append_kernel<__nv_bfloat16, 16, true> : kv_append_kernel<__nv_bfloat16, 16, false>)
+                          : (vec ? kv_append_kernel<__nv_bfloat16, 4, true> : kv_append_kernel<__nv_bfloat16, 4, false>);
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem) != cudaSuccess)
+        return LF_ERR_CUDA;
+    kern<<<grid, kRotThreads, smem, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+}
+
+uint64_t lf_attn_cache_workspace_bytes(int q_heads, int kv_heads, int d) {
+    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (d != 64 && d != 128) || q_heads > kMaxHeads) return 0;
+    const int group = q_heads / kv_heads, nsub = (group + 15) / 16, gs = (group + nsub - 1) / nsub;
+    return uint64_t(2) * kKvGrid * gs * (d + 2) * sizeof(float);
+}
+
+lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, const void* k_cache, const void* v_cache,
+                            const void* k_par, const void* v_par, int n_pages, int page, const int32_t* table,
+                            int max_pages, const void* plan, int n_seqs, int n_tokens, int n_global, int q_heads,
+                            int kv_heads, int d, int r, const int32_t* dil, float scale, lf_dtype dtype, int bits,
+                            void* workspace, uint64_t workspace_bytes, void* stream) {
+    if (!q || !out || !strides || !table || !plan || !workspace || !std::isfinite(scale)) return LF_ERR_INVALID_ARG;
+    if (!aligned(table, 4) || !aligned(plan, 256) || !aligned(workspace, 16)) return LF_ERR_INVALID_ARG;
+    KvShape sh;
+    lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, r, dil, &sh);
+    if (st != LF_OK) return st;
+    if ((st = check_cache(k_cache, v_cache, k_par, v_par, n_pages, kv_heads, page, d, dtype, bits)) != LF_OK) return st;
+    const int64_t n[2] = {n_tokens, q_heads};
+    Span a, b;
+    if (!span_of(q, 2, n, strides, d, 2, &a) || !span_of(out, 2, n, strides + 2, d, 2, &b) ||
+        !distinct(2, n, strides + 2) || !by_eight(q, 2, strides, 2) || !aligned(out, 2) || a.meets(b))
+        return LF_ERR_INVALID_ARG;
+    if (workspace_bytes < lf_attn_cache_workspace_bytes(q_heads, kv_heads, d)) return LF_ERR_SCRATCH_TOO_SMALL;
+    if (n_tokens == 0) return LF_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    KvAttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    int sms = 0;
+    if ((st = device_info(s, &p.status, &sms)) != LF_OK) return st;
+    p.q = q;
+    p.out = out;
+    p.q_row = strides[0];
+    p.q_head = strides[1];
+    p.o_row = strides[2];
+    p.o_head = strides[3];
+    p.k = static_cast<const uint8_t*>(k_cache);
+    p.v = static_cast<const uint8_t*>(v_cache);
+    p.k_par = static_cast<const uint8_t*>(k_par);
+    p.v_par = static_cast<const uint8_t*>(v_par);
+    p.table = table;
+    p.plan = kv_plan_view(const_cast<void*>(plan), kv_plan_layout(n_seqs, n_tokens, n_global));
+    p.part = static_cast<float*>(workspace);
+    p.N = n_tokens;
+    p.n_pages = n_pages;
+    p.log_page = log2_of(page);
+    p.max_pages = max_pages;
+    p.kv_heads = kv_heads;
+    p.group = q_heads / kv_heads;
+    p.nsub = sh.nsub;
+    p.gs = (p.group + p.nsub - 1) / p.nsub;
+    p.r = sh.r;
+    p.n_global = n_global;
+    p.G = sh.G;
+    p.sl2 = static_cast<float>(double(scale) * kLog2e);
+    p.sig = sh.sig_all;
+    std::memcpy(p.dil, sh.dil, sizeof(p.dil));
+    const bool half = dtype == LF_F16, two = p.gs > 8;
+    const AttnKernel kern = d == 64 ? (bits == 16 ? attn_kernel<64, 16>(half, two) : attn_kernel<64, 4>(half, two))
+                                    : (bits == 16 ? attn_kernel<128, 16>(half, two) : attn_kernel<128, 4>(half, two));
+    kern<<<p.G, kKvThreads, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return LF_ERR_CUDA;
+    const AttnKernel merge = d == 64 ? (half ? kv_merge_kernel<64, true> : kv_merge_kernel<64, false>)
+                                     : (half ? kv_merge_kernel<128, true> : kv_merge_kernel<128, false>);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.G);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, merge, p) == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+}
+
+}  // extern "C"

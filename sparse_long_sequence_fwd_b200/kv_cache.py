@@ -1,0 +1,222 @@
+"""The paged key/value cache, of 16 or of 4 bits, and the attention of single tokens over it (``lf_attn_cache_*``).
+
+One step of a model that answers token by token:
+
+    plan = Plan(cache, table, cu_tokens, context, n_tokens, q_heads, r, ...)   # once a step, for all layers
+    q = append(cache, plan, k, v, q=q, freqs=freqs)                            # per layer: keys turned on the way
+    y = fwd(cache, plan, q)
+
+``table``, ``cu_tokens``, ``context`` and ``global_idx`` stay on the device, and ``Plan.refresh`` lays the step out
+again from what they then hold, so a step can be captured into a CUDA graph and replayed.  Work runs in the library's
+kernels only.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import lf_attn
+from .lf_attn import LfAttnError, _dil_array, _dtype_code, _ptr
+from .rotary import _check_freqs, _on
+
+
+def _int32(t: torch.Tensor, shape, what: str) -> torch.Tensor:
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 %s tensor" % (what, list(shape)))
+    return t
+
+
+class KVCache:
+    """The pages of one layer.  16 bits: k, v [pages, kv_heads, page, d] (bfloat16 or float16).  4 bits: k, v
+    [pages, kv_heads, page, d / 2] uint8 codes and k_par, v_par [pages, kv_heads, page, d / 32, 2] float16 (scale,
+    mid) of each group of 32 values, in the order that ``include/lf_attn.h`` describes."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_par: Optional[torch.Tensor] = None,
+                 v_par: Optional[torch.Tensor] = None):
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v must be [pages, kv_heads, page, width] of one dtype")
+        if (k_par is None) != (v_par is None):
+            raise ValueError("k_par and v_par go together")
+        self.pages, self.kv_heads, self.page, width = k.shape
+        self.bits = 16 if k_par is None else 4
+        self.d = width if self.bits == 16 else 2 * width
+        if self.bits == 16 and k.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("a 16-bit cache is bfloat16 or float16")
+        if self.bits == 4:
+            shape = (self.pages, self.kv_heads, self.page, self.d // 32, 2)
+            if k.dtype != torch.uint8:
+                raise TypeError("the codes of a 4-bit cache are uint8")
+            for t in (k_par, v_par):
+                if t.dtype != torch.float16 or tuple(t.shape) != shape:
+                    raise ValueError("k_par and v_par must be float16 %s" % list(shape))
+        for t in (k, v, k_par, v_par):
+            if t is not None and (not t.is_contiguous() or t.device != k.device):
+                raise ValueError("the cache's tensors must be contiguous and on one device")
+        self.k, self.v, self.k_par, self.v_par = k, v, k_par, v_par
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page: int, d: int, dtype: torch.dtype = torch.bfloat16, bits: int = 16,
+              device="cuda") -> "KVCache":
+        """A cache whose pages hold nothing yet.  ``dtype`` counts for 16 bits only."""
+        if bits == 16:
+            return cls(*[torch.empty(pages, kv_heads, page, d, dtype=dtype, device=device) for _ in range(2)])
+        if bits != 4 or d % 32:
+            raise ValueError("bits must be 16 or 4, and d a multiple of 32")
+        codes = [torch.empty(pages, kv_heads, page, d // 2, dtype=torch.uint8, device=device) for _ in range(2)]
+        par = [torch.empty(pages, kv_heads, page, d // 32, 2, dtype=torch.float16, device=device) for _ in range(2)]
+        return cls(*codes, *par)
+
+    def tensors(self):
+        return [t for t in (self.k, self.v, self.k_par, self.v_par) if t is not None]
+
+
+class Plan:
+    """One step over caches shaped as ``cache``: rows [cu_tokens[s], cu_tokens[s+1]) of the step's n_tokens rows are
+    sequence s's new tokens, at positions context[s] on; rows behind the last sequence are no tokens.  ``table``:
+    int32 [n_seqs, max_pages]; ``global_idx``: int32 [n_seqs, n_global], any order; ``dil``: an int or one per kv head;
+    ``r``: how many (dilated) positions back a token sees beside the global ones, None for all of them."""
+
+    def __init__(self, cache: KVCache, table: torch.Tensor, cu_tokens: torch.Tensor, context: torch.Tensor,
+                 n_tokens: int, q_heads: int, r: Optional[int] = None, dil=None,
+                 global_idx: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        if context.dim() != 1 or table.dim() != 2:
+            raise ValueError("context must be [n_seqs] and table [n_seqs, max_pages]")
+        S = context.shape[0]
+        self.n_seqs, self.n_tokens, self.q_heads, self.kv_heads = S, int(n_tokens), int(q_heads), cache.kv_heads
+        self.page, self.max_pages = cache.page, table.shape[1]
+        self.r = (1 << 31) - 1 if r is None else int(r)
+        self.dil = _dil_array(dil, cache.kv_heads)
+        self.table = _int32(table, (S, self.max_pages), "table")
+        self.cu_tokens = _int32(cu_tokens, (S + 1,), "cu_tokens")
+        self.context = _int32(context, (S,), "context")
+        self.n_global = 0 if global_idx is None else global_idx.shape[1]
+        self.global_idx = None
+        if self.n_global:
+            self.global_idx = _int32(global_idx, (S, self.n_global), "global_idx")
+        size = lf_attn.load().lf_attn_cache_plan_bytes(S, self.n_tokens, self.n_global)
+        if size == 0:
+            raise LfAttnError(1, "lf_attn_cache_plan_bytes")
+        stack, _ = _on(stream, self._inputs())
+        with stack:
+            self.buffer = torch.empty(size, dtype=torch.uint8, device=context.device)
+        self.refresh(stream)
+
+    def _inputs(self):
+        return [t for t in (self.cu_tokens, self.context, self.table, self.global_idx) if t is not None]
+
+    def refresh(self, stream: Optional[torch.cuda.Stream] = None) -> "Plan":
+        """Lays the step out again, from what cu_tokens, context and global_idx hold when the call runs."""
+        stack, s = _on(stream, self._inputs() + [self.buffer])
+        with stack:
+            st = lf_attn.load().lf_attn_cache_plan(
+                _ptr(self.cu_tokens), _ptr(self.context), self.n_seqs, self.n_tokens, _ptr(self.global_idx),
+                self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.r, self.dil,
+                _ptr(self.buffer), s)
+        if st != 0:
+            raise LfAttnError(st, "lf_attn_cache_plan")
+        return self
+
+    def _check(self, cache: KVCache):
+        if (cache.kv_heads, cache.page) != (self.kv_heads, self.page):
+            raise ValueError("the plan was made for a cache with other heads or pages")
+
+
+def _rows(t: torch.Tensor, plan: Plan, heads: int, d: int, dtype, what: str) -> torch.Tensor:
+    if tuple(t.shape) != (plan.n_tokens, heads, d):
+        raise ValueError("%s must be [n_tokens, heads, d] = %s" % (what, [plan.n_tokens, heads, d]))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (what, dtype))
+    if t.stride(2) != 1:
+        raise ValueError("the d values of a row of %s must be contiguous" % what)
+    return t
+
+
+def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Optional[torch.Tensor] = None,
+           freqs: Optional[torch.Tensor] = None, interleaved: bool = False, amplitude: float = 1.0,
+           q_out: Optional[torch.Tensor] = None, held=None, stream: Optional[torch.cuda.Stream] = None):
+    """Puts the step's keys (turned by their positions where ``freqs`` is given) and values into the cache, and gives
+    the turned q (None without q).  k, v: [n_tokens, kv_heads, d], q: [n_tokens, q_heads, d], of any strides.
+
+    ``held`` asks for what the cache now holds of these rows, as dense 16-bit rows (for 4 bits the dequantised
+    values): True for new tensors, or the two to write; append then gives (q, k_held, v_held)."""
+    plan._check(cache)
+    dtype = k.dtype
+    code = _dtype_code(k)
+    if cache.bits == 16 and dtype != cache.k.dtype:
+        raise TypeError("rows and cache must share a dtype")
+    _rows(k, plan, cache.kv_heads, cache.d, dtype, "k")
+    _rows(v, plan, cache.kv_heads, cache.d, dtype, "v")
+    if q is not None:
+        _rows(q, plan, plan.q_heads, cache.d, dtype, "q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if q_out is not None:
+        _rows(q_out, plan, plan.q_heads, cache.d, dtype, "q_out")
+    given = held is not None and held is not False and held is not True
+    if given:
+        for t in held:
+            _rows(t, plan, cache.kv_heads, cache.d, dtype, "held")
+        if len(held) != 2:
+            raise ValueError("held must be True or the two tensors to write")
+    rot = _check_freqs(freqs, cache.d)
+    used = [k, v, plan.buffer, plan.table] + cache.tensors() + [t for t in (q, freqs, q_out) if t is not None]
+    stack, s = _on(stream, used + (list(held) if given else []))
+    with stack:
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        if held is True:
+            held = [torch.empty(k.shape, dtype=dtype, device=k.device) for _ in range(2)]
+        hk, hv = held if held is not None and held is not False else (None, None)
+        if plan.n_tokens == 0:  # empty tensors have no address
+            return (q_out, hk, hv) if hk is not None else q_out
+        strides = (ctypes.c_int64 * 12)(*[0 if t is None else t.stride(i) for t in (k, v, q, hk, hv, q_out)
+                                          for i in range(2)])
+        st = lf_attn.load().lf_attn_cache_append(
+            _ptr(k), _ptr(v), _ptr(q), _ptr(hk), _ptr(hv), _ptr(q_out), strides, _ptr(cache.k), _ptr(cache.v),
+            _ptr(cache.k_par), _ptr(cache.v_par), cache.pages, cache.page, _ptr(plan.table), plan.max_pages,
+            _ptr(plan.buffer), plan.n_seqs, plan.n_tokens, plan.n_global, plan.q_heads, cache.kv_heads, cache.d,
+            _ptr(freqs) if rot else None, rot, 1 if interleaved else 0, float(amplitude), code, cache.bits, s)
+    if st != 0:
+        raise LfAttnError(st, "lf_attn_cache_append")
+    return (q_out, hk, hv) if hk is not None else q_out
+
+
+def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = None,
+        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The attention of the step's rows q [n_tokens, q_heads, d] over the cache, which already holds their own keys.
+    Rows behind the last sequence are left as they are in ``out``.  ``workspace``: a uint8 tensor of
+    lf_attn_cache_workspace_bytes for callers that keep one (per stream)."""
+    plan._check(cache)
+    code = _dtype_code(q)
+    if cache.bits == 16 and q.dtype != cache.k.dtype:
+        raise TypeError("q and cache must share a dtype")
+    _rows(q, plan, plan.q_heads, cache.d, q.dtype, "q")
+    if out is not None:
+        _rows(out, plan, plan.q_heads, cache.d, q.dtype, "out")
+    if scale is None:
+        scale = cache.d ** -0.5
+    lib = lf_attn.load()
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    used = [q, plan.buffer, plan.table] + cache.tensors() + [t for t in (out, workspace) if t is not None]
+    stack, s = _on(stream, used)
+    with stack:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if workspace is None:
+            size = lib.lf_attn_cache_workspace_bytes(plan.q_heads, cache.kv_heads, cache.d)
+            workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=q.device)
+        if plan.n_tokens == 0:
+            return out
+        strides = (ctypes.c_int64 * 4)(q.stride(0), q.stride(1), out.stride(0), out.stride(1))
+        st = lib.lf_attn_cache_fwd(
+            _ptr(q), _ptr(out), strides, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_par), _ptr(cache.v_par),
+            cache.pages, cache.page, _ptr(plan.table), plan.max_pages, _ptr(plan.buffer), plan.n_seqs, plan.n_tokens,
+            plan.n_global, plan.q_heads, cache.kv_heads, cache.d, plan.r, plan.dil, float(scale), code, cache.bits,
+            _ptr(workspace), workspace.numel(), s)
+    if st != 0:
+        raise LfAttnError(st, "lf_attn_cache_fwd")
+    return out

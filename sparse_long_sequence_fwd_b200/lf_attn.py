@@ -21,7 +21,9 @@ STATUS = {0: "LF_OK", 1: "LF_ERR_INVALID_ARG", 2: "LF_ERR_UNSUPPORTED", 3: "LF_E
 EXPORTS = ("lf_attn_fwd", "lf_attn_fwd_rand", "lf_attn_bwd", "lf_attn_rows_partial", "lf_attn_merge_rows",
            "lf_attn_fwd_stages", "lf_attn_fwd_host", "lf_attn_device_status", "lf_attn_strerror",
            "lf_attn_release", "lf_attn_workspace_bytes", "lf_attn_last_launch_count",
-           "lf_attn_fwd_static", "lf_attn_band_plan", "lf_attn_test_hooks")
+           "lf_attn_fwd_static", "lf_attn_band_plan", "lf_attn_test_hooks", "lf_attn_rotary",
+           "lf_attn_cache_plan_bytes", "lf_attn_cache_plan", "lf_attn_cache_append",
+           "lf_attn_cache_workspace_bytes", "lf_attn_cache_fwd")
 
 _lib = None
 
@@ -71,7 +73,21 @@ def load():
         lib.lf_attn_band_plan.restype = I
         lib.lf_attn_test_hooks.argtypes = [ctypes.c_uint32, ctypes.c_uint64]
         lib.lf_attn_test_hooks.restype = None
-
+        F, L = ctypes.c_float, ctypes.c_int64
+        lib.lf_attn_rotary.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P, L, P, I, I, I, F, I, I, P]
+        lib.lf_attn_rotary.restype = I
+        lib.lf_attn_cache_plan_bytes.argtypes = [I, I, I]
+        lib.lf_attn_cache_plan_bytes.restype = ctypes.c_uint64
+        lib.lf_attn_cache_plan.argtypes = [P, P, I, I, P, I, I, I, I, I, I, P, P, P]
+        lib.lf_attn_cache_plan.restype = I
+        lib.lf_attn_cache_append.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, P, I, P, I, I, I, I, I, I, P, I, I,
+                                             F, I, I, P]
+        lib.lf_attn_cache_append.restype = I
+        lib.lf_attn_cache_workspace_bytes.argtypes = [I, I, I]
+        lib.lf_attn_cache_workspace_bytes.restype = ctypes.c_uint64
+        lib.lf_attn_cache_fwd.argtypes = [P, P, P, P, P, P, P, I, I, P, I, P, I, I, I, I, I, I, I, P, F, I, I, P,
+                                          ctypes.c_uint64, P]
+        lib.lf_attn_cache_fwd.restype = I
         _lib = lib
     return _lib
 
