@@ -21,8 +21,11 @@
 //   (movmatrix) per 8 keys.
 // A CTA's four warps take 16 keys each of a 64-key block; a warp keeps its own
 // running maximum, sum and O, joined through shared memory when the unit's
-// piece ends.  The next block's rows are in flight while one is computed, and
-// the page table is read a block before that.
+// piece ends.  Each warp has a ring of kStages 16-key stages in shared memory
+// that it fills itself with cp.async, two blocks ahead of the one it computes,
+// across unit boundaries too (short windows are a few blocks long); the page
+// table is read one block before that, and the next unit's queries while the
+// last block of a unit is computed.
 //
 // 4 bits: a group of 32 values is mid + scale (c - 8).  c - 8 is exact in bf16
 // and f16, so the MMAs run on the codes: q . k = sum over groups of
@@ -43,7 +46,22 @@ namespace lf {
 
 constexpr int kKvWarps = 4;
 constexpr int kKvThreads = kKvWarps * 32;
-constexpr int kKvCtasPerSm = 4;
+constexpr int kStages = 3;
+
+// CTAs of four warps that an SM holds at once: by the ring's shared memory
+// (16-bit d = 64: 48 KB, d = 128: 96 KB a CTA), else by registers.
+__host__ __device__ constexpr int kv_ctas_per_sm(int d, int bits, bool two) {
+    return d == 64 ? (two ? 3 : 4) : (bits == 16 || two ? 2 : 3);
+}
+
+// A stage: the 16 K rows, the 16 V rows, and for 4 bits their parameters.
+template <int HD, int kBits>
+struct KvStage {
+    static constexpr int kRow = kBits == 16 ? HD * 2 : HD / 2;
+    static constexpr int kPar = kBits == 16 ? 0 : HD / 8;
+    static constexpr int kV = 16 * kRow, kKp = 32 * kRow, kVp = kKp + 16 * kPar;
+    static constexpr int kBytes = kVp + 16 * kPar;
+};
 
 struct KvAttnParams {
     const void* q;       // rows [N][q_heads][d], strides in elements
@@ -102,77 +120,116 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t x) {
     }
 }
 
-// What a lane holds of a warp's 16 keys.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {  // zeros if not there
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// 16-bit rows: 16-byte chunk x of row r is at chunk x ^ swz(r), so that the K
+// reads (rows g, chunks c of 8 lanes: two rows, four chunks) and the V reads
+// (rows 2c, chunks g: four rows, two chunks) both meet all 32 banks once.
+__device__ __forceinline__ int swz(int r) { return (((r ^ (r >> 2)) & 1) << 2) | (r & 2); }
+// 4-bit V rows: key k's place, so that keys 2c (2c + 1, ..) are beside each other.
+__device__ __forceinline__ int v_place(int k) { return (k & 8) | ((k & 1) << 2) | ((k >> 1) & 3); }
+
+// Starts the copies of a warp's 16 keys into a stage; lane i (and i + 16)
+// has key i's row of the cache, -1: none (zeros).
+template <int HD, int kBits>
+__device__ __forceinline__ void kv_issue(const KvAttnParams& p, uint32_t stage, int row, int lane) {
+    using St = KvStage<HD, kBits>;
+    constexpr int kChunks = St::kRow / 16;  // per row: 2, 4, 8 or 16
+    if constexpr (kBits == 16) {
+#pragma unroll
+        for (int i = 0; i < kChunks / 2; ++i) {  // 32 lanes take 32 / kChunks rows at a time
+            const int r = (i * 32 + lane) / kChunks, x = lane % kChunks;
+            const int at = __shfl_sync(~0u, row, r);
+            const int64_t off = at < 0 ? 0 : int64_t(at) * St::kRow + 16 * x;
+            const uint32_t dst = stage + r * St::kRow + 16 * (x ^ swz(r));
+            cp_async16(dst, p.k + off, at >= 0);
+            cp_async16(dst + St::kV, p.v + off, at >= 0);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kChunks / 2; ++i) {
+            const int r = (i * 32 + lane) / kChunks, x = lane % kChunks;
+            const int at = __shfl_sync(~0u, row, r);
+            const int64_t off = at < 0 ? 0 : int64_t(at) * St::kRow + 16 * x;
+            cp_async16(stage + r * St::kRow + 16 * x, p.k + off, at >= 0);
+            cp_async16(stage + St::kV + v_place(r) * St::kRow + 16 * x, p.v + off, at >= 0);
+        }
+        const int r = lane & 15;  // lanes 0..15: K parameters, 16..31: V's
+        const uint8_t* src = (lane < 16 ? p.k_par : p.v_par) + (row < 0 ? 0 : int64_t(row) * St::kPar);
+        const uint32_t dst = stage + (lane < 16 ? St::kKp : St::kVp) + r * St::kPar;
+        if constexpr (St::kPar == 16) cp_async16(dst, src, row >= 0);
+        else cp_async8(dst, src, row >= 0);
+    }
+}
+
+// What a lane takes of a stage.
 template <int HD, int kBits>
 struct KvRegs;
 template <int HD>
 struct KvRegs<HD, 16> {
     uint4 k[2][HD / 32];  // keys g, g + 8: chunks c, c + 4, ..
     uint4 v[4][HD / 64];  // keys 2c, 2c + 1, 2c + 8, 2c + 9: chunks g, g + 8
-};
-template <int HD>
-struct KvRegs<HD, 4> {
-    uint32_t k[2][HD / 32];   // keys g, g + 8: word [c] of each group
-    uint32_t v[4][HD / 64];   // keys 2c, ..: units [g] of two groups each
-    uint32_t kp[2][HD / 32];  // keys g, g + 8: (scale, mid) of each group
-    uint32_t vp[2][HD / 32];
-};
-
-template <int HD>
-__device__ __forceinline__ void kv_load(KvRegs<HD, 16>& x, const KvAttnParams& p, int row, int lane) {
-    const int g = lane >> 2, c = lane & 3;
+    __device__ __forceinline__ void load_k(const uint8_t* s, int g, int c) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = __shfl_sync(~0u, row, g + 8 * i);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < HD / 32; ++j)
-            x.k[i][j] = at < 0 ? make_uint4(0, 0, 0, 0)
-                               : __ldg(reinterpret_cast<const uint4*>(p.k + int64_t(at) * (HD * 2)) + c + 4 * j);
+            for (int j = 0; j < HD / 32; ++j)
+                k[i][j] = *reinterpret_cast<const uint4*>(s + (g + 8 * i) * (HD * 2) + 16 * ((c + 4 * j) ^ swz(g + 8 * i)));
     }
+    __device__ __forceinline__ void load_v(const uint8_t* s, int g, int c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = __shfl_sync(~0u, row, 2 * c + (i & 1) + 8 * (i >> 1));
+        for (int i = 0; i < 4; ++i) {
+            const int r = 2 * c + (i & 1) + 8 * (i >> 1);
 #pragma unroll
-        for (int j = 0; j < HD / 64; ++j)
-            x.v[i][j] = at < 0 ? make_uint4(0, 0, 0, 0)
-                               : __ldg(reinterpret_cast<const uint4*>(p.v + int64_t(at) * (HD * 2)) + g + 8 * j);
+            for (int j = 0; j < HD / 64; ++j)
+                v[i][j] = *reinterpret_cast<const uint4*>(s + KvStage<HD, 16>::kV + r * (HD * 2) + 16 * ((g + 8 * j) ^ swz(r)));
+        }
     }
-}
-
+};
 template <int W>
-__device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t* at, bool there) {
+__device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t* at) {
     static_assert(W == 1 || W == 2 || W == 4, "");
-    if (!there) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) x[i] = 0;
-    } else if constexpr (W == 1) {
-        x[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+    if constexpr (W == 1) {
+        x[0] = *reinterpret_cast<const uint32_t*>(at);
     } else if constexpr (W == 2) {
-        const uint2 t = __ldg(reinterpret_cast<const uint2*>(at));
+        const uint2 t = *reinterpret_cast<const uint2*>(at);
         x[0] = t.x; x[1] = t.y;
     } else {
-        const uint4 t = __ldg(reinterpret_cast<const uint4*>(at));
+        const uint4 t = *reinterpret_cast<const uint4*>(at);
         x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
     }
 }
-
 template <int HD>
-__device__ __forceinline__ void kv_load(KvRegs<HD, 4>& x, const KvAttnParams& p, int row, int lane) {
-    constexpr int kGroups = HD / 32;
-    const int g = lane >> 2, c = lane & 3;
+struct KvRegs<HD, 4> {
+    static constexpr int kGroups = HD / 32;
+    using St = KvStage<HD, 4>;
+    uint32_t k[2][kGroups];   // keys g, g + 8: word [c] of each group
+    uint32_t v[4][HD / 64];   // keys 2c, ..: units [g] of two groups each
+    uint32_t kp[2][kGroups];  // keys g, g + 8: (scale, mid) of each group
+    uint32_t vp[2][kGroups];
+    __device__ __forceinline__ void load_k(const uint8_t* s, int g, int c) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = __shfl_sync(~0u, row, g + 8 * i);
-        load_words(x.k[i], p.k + int64_t(at) * (HD / 2) + c * (4 * kGroups), at >= 0);
-        load_words(x.kp[i], p.k_par + int64_t(at) * (4 * kGroups), at >= 0);
-        load_words(x.vp[i], p.v_par + int64_t(at) * (4 * kGroups), at >= 0);
+        for (int i = 0; i < 2; ++i) {
+            load_words(k[i], s + (g + 8 * i) * St::kRow + c * (4 * kGroups));
+            load_words(kp[i], s + St::kKp + (g + 8 * i) * St::kPar);
+        }
     }
+    __device__ __forceinline__ void load_v(const uint8_t* s, int g, int c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = __shfl_sync(~0u, row, 2 * c + (i & 1) + 8 * (i >> 1));
-        load_words(x.v[i], p.v + int64_t(at) * (HD / 2) + g * (2 * kGroups), at >= 0);
+        for (int i = 0; i < 2; ++i) load_words(vp[i], s + St::kVp + (g + 8 * i) * St::kPar);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            load_words(v[i], s + St::kV + v_place(2 * c + (i & 1) + 8 * (i >> 1)) * St::kRow + g * (2 * kGroups));
     }
-}
+};
 
 __device__ __forceinline__ float2 par_of(uint32_t x) {  // (scale, mid)
     return __half22float2(*reinterpret_cast<const __half2*>(&x));
@@ -191,15 +248,26 @@ struct KvState {
     float qs[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2];  // sums of q over a group
     float om[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2];  // sums of p mid
 
-    __device__ __forceinline__ void begin(const KvAttnParams& p, const uint8_t* qrow, int heads, int lane) {
+    // The unit's queries as they are in memory: lane (g, c) takes chunks c, c + 4, .. of query head 8 n + g.
+    static __device__ __forceinline__ void load_q(uint4 (&x)[kNt][HD / 32], const KvAttnParams& p, const uint8_t* qrow,
+                                                  int heads, int lane) {
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int j = 0; j < HD / 32; ++j)
+                x[n][j] = 8 * n + g < heads
+                              ? __ldg(reinterpret_cast<const uint4*>(qrow + 2 * p.q_head * (8 * n + g)) + c + 4 * j)
+                              : make_uint4(0, 0, 0, 0);
+    }
+
+    __device__ __forceinline__ void begin(const uint4 (&x)[kNt][HD / 32], int lane) {
+        const int c = lane & 3;
+#pragma unroll
         for (int n = 0; n < kNt; ++n) {
-            const bool there = 8 * n + g < heads;
-            const uint8_t* at = qrow + 2 * p.q_head * (8 * n + g);
 #pragma unroll
             for (int j = 0; j < HD / 32; ++j) {
-                const uint4 t = there ? __ldg(reinterpret_cast<const uint4*>(at) + c + 4 * j) : make_uint4(0, 0, 0, 0);
+                const uint4 t = x[n][j];
                 if constexpr (kBits == 16) {
                     q[n][2 * j][0] = t.x; q[n][2 * j][1] = t.y;
                     q[n][2 * j + 1][0] = t.z; q[n][2 * j + 1][1] = t.w;
@@ -233,8 +301,10 @@ struct KvState {
         }
     }
 
-    // One step over the warp's 16 keys; ok0, ok1: keys g and g + 8 are keys.
-    __device__ __forceinline__ void step(const KvRegs<HD, kBits>& x, bool ok0, bool ok1, float sl2) {
+    // One step over the 16 keys of a stage; ok0, ok1: keys g and g + 8 are keys.
+    __device__ __forceinline__ void step(const uint8_t* stage, int g, int c, bool ok0, bool ok1, float sl2) {
+        KvRegs<HD, kBits> x;
+        x.load_k(stage, g, c);
         float s[kNt][4];
         if constexpr (kBits == 16) {
 #pragma unroll
@@ -313,6 +383,7 @@ struct KvState {
                 l[n][i & 1] += s[n][i];
             }
         }
+        x.load_v(stage, g, c);
         if constexpr (kBits == 16) {
             uint32_t b[kNt][2];
 #pragma unroll
@@ -381,31 +452,64 @@ struct KvState {
     }
 };
 
-// The row of the cache that key i (0..15, lanes 16..31 repeat them) of this
-// warp's part of block b is in, -1 if there is no such key.
-__device__ __forceinline__ int kv_row(const KvAttnParams& p, const KvKeys& u, int seq, int pos, int head, int b, int warp,
-                                      int lane) {
-    const int i = 16 * warp + (lane & 15);
-    int at = -1;
-    if (b < u.blocks_win) {
-        const int n = b * kKvBlock + i;
-        if (n < u.n_win) at = u.first + n * u.step;
-    } else {
-        const int n = (b - u.blocks_win) * kKvBlock + i;
-        if (n < u.ng) {
-            at = p.plan.g_list[int64_t(seq) * p.n_global + n];
-            const int back = pos - at;  // > 0
-            if (back % u.step == 0 && back / u.step < u.n_win) at = -1;  // in the window
+// Where a CTA is in its range of the work sequence; all warps walk alike.
+struct KvWalk {
+    int row, unit, seq, pos, ng, head;
+    int b, b1, nb;   // the next block of the unit, and where the CTA's piece of it ends
+    int64_t left;    // blocks of the range from block b on
+    KvKeys u;
+
+    __device__ __forceinline__ void enter(const KvAttnParams& p) {
+        head = unit / p.nsub;
+        u = KvKeys(pos, ng, p.r, p.dil[head]);
+        nb = u.blocks();
+        b1 = static_cast<int>(min(int64_t(nb), b + left));
+    }
+    __device__ __forceinline__ KvWalk(const KvAttnParams& p, const KvStart& s)
+        : row(s.row), unit(s.unit), seq(s.seq), pos(s.pos), ng(s.ng), b(s.blk), left(s.n), u(s.pos, s.ng, p.r, 1) {
+        enter(p);
+    }
+    __device__ __forceinline__ void next_unit(const KvAttnParams& p) {
+        b = 0;
+        if (++unit == p.kv_heads * p.nsub) {
+            unit = 0;
+            do ++row;
+            while (row < p.N && p.plan.row_seq[row] < 0);  // rows without keys
+            if (row >= p.N) {
+                left = 0;
+                return;
+            }
+            seq = p.plan.row_seq[row];
+            pos = p.plan.row_pos[row];
+            ng = p.plan.row_ng[row];
         }
+        enter(p);
     }
-    if (at < 0) return -1;
-    const int page = p.table[int64_t(seq) * p.max_pages + (at >> p.log_page)];
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
-        atomicOr(p.status, kStatusBadCache);
-        return -1;
+
+    // The row of the cache that key i = lane & 15 of the warp's part of block b is in, -1 if there is no such key.
+    __device__ __forceinline__ int key_row(const KvAttnParams& p, int warp, int lane) const {
+        const int i = 16 * warp + (lane & 15);
+        int at = -1;
+        if (b < u.blocks_win) {
+            const int n = b * kKvBlock + i;
+            if (n < u.n_win) at = u.first + n * u.step;
+        } else {
+            const int n = (b - u.blocks_win) * kKvBlock + i;
+            if (n < u.ng) {
+                at = p.plan.g_list[int64_t(seq) * p.n_global + n];
+                const int back = pos - at;  // > 0
+                if (back % u.step == 0 && back / u.step < u.n_win) at = -1;  // in the window
+            }
+        }
+        if (at < 0) return -1;
+        const int page = p.table[int64_t(seq) * p.max_pages + (at >> p.log_page)];
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
+            atomicOr(p.status, kStatusBadCache);
+            return -1;
+        }
+        return ((page * p.kv_heads + head) << p.log_page) + (at & ((1 << p.log_page) - 1));
     }
-    return ((page * p.kv_heads + head) << p.log_page) + (at & ((1 << p.log_page) - 1));
-}
+};
 
 template <bool kHalf>
 __device__ __forceinline__ void store16(void* at, int64_t i, float x) {
@@ -413,160 +517,239 @@ __device__ __forceinline__ void store16(void* at, int64_t i, float x) {
     else static_cast<__nv_bfloat16*>(at)[i] = __float2bfloat16_rn(x);
 }
 
+// Floats of a partial state: O, m and l of each query head of a unit.
+__host__ __device__ constexpr int kv_piece_row(int d) { return d + 2; }
+
+// The warps' rings, and room to join 8 query heads' 64 dimensions of the four warps at a time.
+constexpr int kJoinRow = 68;
+template <int HD, int kBits>
+constexpr int kv_attn_smem(int gs) {
+    return kKvWarps * (kStages * KvStage<HD, kBits>::kBytes + (gs < 8 ? gs : 8) * kJoinRow * 4);
+}
+
 template <int HD, int kBits, bool kHalf, int kNt>
-__global__ void __launch_bounds__(kKvThreads) kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
+__global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2))
+    kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
     constexpr int kRows = 8 * kNt;
-    __shared__ float s_o[kKvWarps][kRows][HD + 4];
+    constexpr int kStage = KvStage<HD, kBits>::kBytes;
+    constexpr int kUnits = 8;  // descriptors in flight: at most kStages + 2 units are between the walk and the end
+    using State = KvState<HD, kBits, kHalf, kNt>;
+    extern __shared__ __align__(128) uint8_t s_ring[];
+    float* s_o = reinterpret_cast<float*>(s_ring + kKvWarps * kStages * kStage);
     __shared__ float s_m[kKvWarps][kRows], s_l[kKvWarps][kRows];
+    __shared__ int4 s_unit[kKvWarps][kUnits];  // row, unit, -, slot of its partial state (-1: whole)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int s = blockIdx.x;
     grid_dep_launch();
+    const KvStart start = p.plan.start[s];
     if (p.plan.sig[1] != p.sig) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadPlan);
         return;
     }
-    const int64_t W = p.plan.total[0], G = W < p.G ? W : p.G;
-    if (s >= G) return;
-    int64_t left = (s + 1) * W / G - s * W / G;
-    KvStart at = p.plan.start[s];
-    bool first_piece = true;
-    const int units = p.kv_heads * p.nsub;
-    while (left > 0 && at.row < p.N) {
-        const int seq = p.plan.row_seq[at.row];
-        if (seq < 0) {  // a row without keys
-            ++at.row;
-            continue;
-        }
-        const int pos = p.plan.row_pos[at.row], ng = p.plan.row_ng[at.row];
-        const int head = at.unit / p.nsub, sub = at.unit - head * p.nsub;
-        const int heads = min(p.gs, p.group - sub * p.gs), qh = head * p.group + sub * p.gs;
-        const KvKeys u(pos, ng, p.r, p.dil[head]);
-        const int nb = u.blocks();
-        const int b0 = at.blk, b1 = static_cast<int>(min(int64_t(nb), b0 + left));
+    if (start.n <= 0) return;
+    uint8_t* ring = s_ring + warp * (kStages * kStage);
+    const uint32_t ring_at = smem_u32(ring);
 
-        KvState<HD, kBits, kHalf, kNt> st;
-        st.begin(p, static_cast<const uint8_t*>(p.q) + 2 * (at.row * p.q_row + qh * p.q_head), heads, lane);
-        KvRegs<HD, kBits> x[2];
-        int row[2];
-        row[0] = kv_row(p, u, seq, pos, head, b0, warp, lane);
-        kv_load(x[0], p, row[0], lane);
-        row[1] = b0 + 1 < b1 ? kv_row(p, u, seq, pos, head, b0 + 1, warp, lane) : -1;
-        for (int b = b0; b < b1; b += 2) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (b + e >= b1) break;
-                const int now = row[e];
-                if (b + e + 1 < b1) kv_load(x[1 - e], p, row[1 - e], lane);
-                row[e] = b + e + 2 < b1 ? kv_row(p, u, seq, pos, head, b + e + 2, warp, lane) : -1;
-                const unsigned ok = __ballot_sync(~0u, now >= 0);
-                if (ok) st.step(x[e], (ok >> g) & 1, (ok >> (g + 8)) & 1, p.sl2);
-            }
+    // The walk runs ahead of the blocks that are computed.  A block's meta:
+    // bits 0-15 which keys there are, bit 16 first and bit 17 last of its piece, bits 20.. the unit's descriptor.
+    KvWalk w(p, start);
+    int entered = 0;
+    auto describe = [&](bool first_piece) {
+        const bool whole = w.b == 0 && w.b1 == w.nb;
+        // slot 2s: the piece a CTA begins with, of a unit that an earlier one began; 2s + 1: one that a later CTA ends
+        if (lane == 0)
+            s_unit[warp][entered % kUnits] = make_int4(w.row, w.unit, 0, whole ? -1 : 2 * s + (first_piece && w.b > 0 ? 0 : 1));
+    };
+    int row_next = -1;
+    uint32_t meta_next = 0;
+    bool fresh = true;
+    describe(true);
+    auto fetch = [&] {
+        row_next = -1;
+        meta_next = 0;
+        if (w.left <= 0) return;
+        row_next = w.key_row(p, warp, lane);
+        meta_next = (fresh ? 1u << 16 : 0u) | (w.b + 1 == w.b1 ? 1u << 17 : 0u) | uint32_t(entered % kUnits) << 20;
+        fresh = false;
+        --w.left;
+        if (++w.b == w.b1 && w.left > 0) {
+            w.next_unit(p);
+            ++entered;
+            fresh = true;
+            describe(false);
         }
-        // join the lanes' and the warps' states
+    };
+    uint32_t meta[kStages];
+    int64_t todo = start.n;
+    auto issue = [&](int stage, uint32_t& m) {
+        kv_issue<HD, kBits>(p, ring_at + stage * kStage, row_next, lane);
+        cp_async_commit();
+        m = meta_next | (__ballot_sync(~0u, row_next >= 0) & 0xffffu);
+    };
+    fetch();
 #pragma unroll
-        for (int n = 0; n < kNt; ++n)
+    for (int i = 0; i < kStages - 1; ++i) {
+        issue(i, meta[i]);
+        fetch();
+    }
+    auto query = [&](uint4 (&x)[kNt][HD / 32], uint32_t m) {
+        const int4 d = s_unit[warp][m >> 20];
+        const int head = d.y / p.nsub, sub = d.y - head * p.nsub;
+        State::load_q(x, p, static_cast<const uint8_t*>(p.q) + 2 * (d.x * p.q_row + (head * p.group + sub * p.gs) * p.q_head),
+                      min(p.gs, p.group - sub * p.gs), lane);
+    };
+    State st;
+    uint4 qn[kNt][HD / 32];
+    __syncwarp();
+    query(qn, meta[0]);
+    int stage = 0;
+    for (; todo > 0; --todo) {
+        __syncwarp();  // every lane has read the stage that is filled next
+        issue(stage == 0 ? kStages - 1 : stage - 1, meta[kStages - 1]);
+        fetch();
+        const uint32_t now = meta[0];
+        if (now & (1u << 16)) st.begin(qn, lane);
+        __syncwarp();
+        if (meta[1] & (1u << 16)) query(qn, meta[1]);
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        if (now & 0xffffu) st.step(ring + stage * kStage, g, c, (now >> g) & 1, (now >> (g + 8)) & 1, p.sl2);
+        if (now & (1u << 17)) {  // join the lanes' and the warps' states
+            const int4 d = s_unit[warp][now >> 20];
+            const int head = d.y / p.nsub, sub = d.y - head * p.nsub;
+            const int heads = min(p.gs, p.group - sub * p.gs), qh = head * p.group + sub * p.gs;
+const int join = min(p.gs, 8) * kJoinRow;  // floats of a warp
+            float* part = p.part + int64_t(d.w) * p.gs * kv_piece_row(HD);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float l = st.l[n][e];
-                l += __shfl_xor_sync(~0u, l, 4);
-                l += __shfl_xor_sync(~0u, l, 8);
-                l += __shfl_xor_sync(~0u, l, 16);
-                const int h = 8 * n + 2 * c + e;
-                if (g == 0) {
-                    s_m[warp][h] = st.m[n][e];
-                    s_l[warp][h] = l;
-                }
-                if constexpr (kBits == 4) {
+            for (int n = 0; n < kNt; ++n) {
 #pragma unroll
-                    for (int j = 0; j < HD / 32; ++j) {
-                        float t = st.om[n][j][e];
-                        t += __shfl_xor_sync(~0u, t, 4);
-                        t += __shfl_xor_sync(~0u, t, 8);
-                        t += __shfl_xor_sync(~0u, t, 16);
+                for (int e = 0; e < 2; ++e) {
+                    float l = st.l[n][e];
+                    l += __shfl_xor_sync(~0u, l, 4);
+                    l += __shfl_xor_sync(~0u, l, 8);
+                    l += __shfl_xor_sync(~0u, l, 16);
+                    if (g == 0) {
+                        s_m[warp][8 * n + 2 * c + e] = st.m[n][e];
+                        s_l[warp][8 * n + 2 * c + e] = l;
+                    }
+                    if constexpr (kBits == 4) {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            st.o[n][2 * j + k][e] += t;
-                            st.o[n][2 * j + k][2 + e] += t;
+                        for (int j = 0; j < HD / 32; ++j) {
+                            float t = st.om[n][j][e];
+                            t += __shfl_xor_sync(~0u, t, 4);
+                            t += __shfl_xor_sync(~0u, t, 8);
+                            t += __shfl_xor_sync(~0u, t, 16);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                st.o[n][2 * j + k][e] += t;
+                                st.o[n][2 * j + k][2 + e] += t;
+                            }
                         }
                     }
                 }
-                if (h < heads)
 #pragma unroll
-                    for (int t = 0; t < HD / 16; ++t) {
-                        s_o[warp][h][st.dim_of(t, 0, g)] = st.o[n][t][e];
-                        s_o[warp][h][st.dim_of(t, 2, g)] = st.o[n][t][2 + e];
+                for (int half = 0; half < HD / 64; ++half) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (8 * n + 2 * c + e < heads)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) {
+                                float* at = s_o + warp * join + (2 * c + e) * kJoinRow;
+                                at[State::dim_of(t, 0, g)] = st.o[n][4 * half + t][e];
+                                at[State::dim_of(t, 2, g)] = st.o[n][4 * half + t][2 + e];
+                            }
+                    __syncthreads();
+                    for (int i = threadIdx.x; i < 64 * min(8, heads - 8 * n); i += kKvThreads) {
+                        const int h = 8 * n + i / 64, e = 64 * half + i % 64;
+                        float m = s_m[0][h];
+#pragma unroll
+                        for (int a = 1; a < kKvWarps; ++a) m = fmaxf(m, s_m[a][h]);
+                        float l = 0.f, o = 0.f;
+#pragma unroll
+                        for (int a = 0; a < kKvWarps; ++a) {
+                            // a warp without keys has m = -inf and zeros
+                            const float f = s_m[a][h] == m ? 1.f : ex2_approx(s_m[a][h] - m);
+                            l += s_l[a][h] * f;
+                            o += s_o[a * join + (i / 64) * kJoinRow + i % 64] * f;
+                        }
+                        if (d.w < 0) {
+                            store16<kHalf>(p.out, d.x * p.o_row + (qh + h) * p.o_head + e, l == 0.f ? 0.f : o / l);
+                        } else {
+                            float* at = part + h * kv_piece_row(HD);
+                            at[e] = o;
+                            if (e == 0) {
+                                at[HD] = m;
+                                at[HD + 1] = l;
+                            }
+                        }
                     }
-            }
-        __syncthreads();
-        const bool whole = b0 == 0 && b1 == nb;
-        // slot 2s: the piece a CTA begins with, of a unit that an earlier one began; 2s + 1: one that a later CTA ends
-        float* part = p.part + (int64_t(2 * s) + (first_piece && b0 > 0 ? 0 : 1)) * p.gs * (HD + 2);
-        for (int i = threadIdx.x; i < heads * HD; i += kKvThreads) {
-            const int h = i / HD, e = i % HD;
-            float m = s_m[0][h];
-#pragma unroll
-            for (int w = 1; w < kKvWarps; ++w) m = fmaxf(m, s_m[w][h]);
-            float l = 0.f, o = 0.f;
-#pragma unroll
-            for (int w = 0; w < kKvWarps; ++w) {
-                // a warp without keys has m = -inf and zeros
-                const float f = s_m[w][h] == m ? 1.f : ex2_approx(s_m[w][h] - m);
-                l += s_l[w][h] * f;
-                o += s_o[w][h][e] * f;
-            }
-            if (whole) {
-                store16<kHalf>(p.out, at.row * p.o_row + (qh + h) * p.o_head + e, l == 0.f ? 0.f : o / l);
-            } else {
-                part[h * (HD + 2) + e] = o;
-                if (e == 0) {
-                    part[h * (HD + 2) + HD] = m;
-                    part[h * (HD + 2) + HD + 1] = l;
+                    __syncthreads();
                 }
             }
         }
-        __syncthreads();
-        left -= b1 - b0;
-        first_piece = false;
-        at.blk = 0;
-        if (++at.unit == units) {
-            at.unit = 0;
-            ++at.row;
-        }
+#pragma unroll
+        for (int i = 0; i + 1 < kStages; ++i) meta[i] = meta[i + 1];
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    cp_async_wait<0>();
 }
 
 // Joins the pieces of the unit that CTA s of the attention began and CTA
-// cut.last ended, in CTA order.  grid: G; the attention's programmatic
-// dependent.
+// cut.last ended, in CTA order.  grid: (G, query heads of a unit), HD
+// threads, one per dimension; the attention's programmatic dependent.
 template <int HD, bool kHalf>
-__global__ void __launch_bounds__(128) kv_merge_kernel(const __grid_constant__ KvAttnParams p) {
-    const int s = blockIdx.x;
-    grid_dep_wait();
-    if (p.plan.sig[1] != p.sig) return;
+__global__ void __launch_bounds__(HD) kv_merge_kernel(const __grid_constant__ KvAttnParams p) {
+    __shared__ float s_w[HD], s_red[2];
+    const int s = blockIdx.x, h = blockIdx.y, e = threadIdx.x;
     const KvCut cut = p.plan.cut[s];
-    if (cut.last < 0) return;
+    const bool mine = cut.last >= 0 && p.plan.sig[1] == p.sig;
+    grid_dep_wait();
+    if (!mine) return;
     const int head = cut.unit / p.nsub, sub = cut.unit - head * p.nsub;
     const int heads = min(p.gs, p.group - sub * p.gs), qh = head * p.group + sub * p.gs;
-    const int64_t piece = int64_t(p.gs) * (HD + 2);
-    const float* first = p.part + (2 * int64_t(s) + 1) * piece;
-    const float* rest = p.part + 2 * int64_t(s + 1) * piece;  // every second slot
-    const int n = cut.last - s;
-    for (int i = threadIdx.x; i < heads * HD; i += 128) {
-        const int h = i / HD, e = i % HD;
-        const float* a = first + h * (HD + 2);
-        float m = a[HD], l = a[HD + 1], o = a[e];
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float* b = rest + 2 * k * piece + h * (HD + 2);
-            const float mb = b[HD], lb = b[HD + 1], ob = b[e];
-            const float t = fmaxf(m, mb);
-            const float fa = m == t ? 1.f : ex2_approx(m - t), fb = mb == t ? 1.f : ex2_approx(mb - t);
-            l = l * fa + lb * fb;
-            o = o * fa + ob * fb;
-            m = t;
+    if (h >= heads) return;
+    // piece 0 is in slot 2s + 1, piece k > 0 in slot 2 (s + k)
+    const int64_t row = kv_piece_row(HD), piece = p.gs * row;
+    const float* base = p.part + 2 * int64_t(s) * piece + h * row;
+    const int n = cut.last - s + 1;
+    float M = -INFINITY, L = 0.f, O = 0.f;
+    for (int k0 = 0; k0 < n; k0 += HD) {  // HD pieces at a time
+        const int k = k0 + e;
+        const float* a = base + (k == 0 ? piece : 2 * k * piece);
+        const float m = k < n ? __ldcg(a + HD) : -INFINITY, l = k < n ? __ldcg(a + HD + 1) : 0.f;
+        float t = m;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
+        if (e == 0) s_red[0] = M;
+        __syncthreads();
+        s_w[e] = t;  // each warp's maximum, in all its lanes' places
+        __syncthreads();
+        float top = s_red[0];
+#pragma unroll
+        for (int a = 0; a < HD / 32; ++a) top = fmaxf(top, s_w[32 * a]);
+        __syncthreads();
+        const float f = m == top ? 1.f : ex2_approx(m - top);
+        s_w[e] = k < n ? f : 0.f;
+        float ls = k < n ? l * f : 0.f;
+        const float old = M == top ? 1.f : ex2_approx(M - top);
+        O *= old;
+        L *= old;
+        M = top;
+        __syncthreads();
+        const int cnt = min(HD, n - k0);
+#pragma unroll 8
+        for (int i = 0; i < cnt; ++i) {
+            const int kk = k0 + i;
+            O += s_w[i] * __ldcg(base + (kk == 0 ? piece : 2 * kk * piece) + e);
         }
-        store16<kHalf>(p.out, cut.row * p.o_row + (qh + h) * p.o_head + e, l == 0.f ? 0.f : o / l);
+        // the sum, over the threads in a fixed order
+        __syncthreads();
+        s_w[e] = ls;
+        __syncthreads();
+        for (int i = 0; i < cnt; ++i) L += s_w[i];
+        __syncthreads();
     }
+    store16<kHalf>(p.out, cut.row * p.o_row + (qh + h) * p.o_head + e, L == 0.f ? 0.f : O / L);
 }
 
 }  // namespace lf

@@ -6,11 +6,17 @@
 //
 // The work sequence: token rows in order; per row its units, one per kv head
 // and group of at most 16 query heads of it; per unit its 64-key blocks, the
-// window's first, then those of the sequence's global list.  CTA s of G takes
-// blocks [s W / G', (s + 1) W / G') of all W, G' = min(G, W), so every CTA has the same number
+// window's first, then those of the sequence's global list.  CTA s of G' takes
+// blocks [s W / G', (s + 1) W / G') of all W, so every CTA has the same number
 // of blocks, give or take one, however ragged the lengths are.  A unit that a
 // range boundary cuts leaves a partial state in every CTA that has a piece of
-// it, and one CTA of the merge kernel joins them.
+// it, and a merge kernel joins them.  G' = min(G, ceil(W / 4)): a CTA's start
+// and a piece's end cost as much as a few blocks.
+//
+// When no ordinary unit has more than kKvWholeBlocks blocks (a window, known
+// on the host), units stay whole: a CTA takes the units that begin in its
+// range, and nothing is merged.  (A global row, which sees every key, is then
+// one CTA's work too.)
 //
 // Bound: latency (a few KB).  The global lists take one CTA per sequence; the
 // rows, their prefix sum and the split one CTA in all, since each needs the
@@ -24,6 +30,8 @@ namespace lf {
 constexpr int kKvBlock = 64;           // keys per block of the work sequence
 constexpr int kKvMaxGlobal = 1024;     // global tokens per sequence (the lists are ranked in O(n^2))
 constexpr int kKvMaxCtas = 2048;
+constexpr int kKvMinBlocks = 4;        // blocks per CTA below which fewer CTAs take part
+constexpr int kKvWholeBlocks = 16;
 constexpr int kPlanThreads = 1024;
 constexpr uint32_t kStatusBadCache = 4u;  // a row or page of a cache call outside its range (left out)
 constexpr uint32_t kStatusBadPlan = 8u;   // a cache call with another plan than its arguments say
@@ -33,13 +41,13 @@ struct KvCut {
     int32_t last;       // its last CTA; -1: CTA s begins no such unit
     int32_t pad;
 };
-struct KvStart {
-    int32_t row, unit, blk, pad;
+struct KvStart {  // where a CTA's range starts, with the row's entries
+    int32_t row, unit, blk, seq, pos, ng;
+    int64_t n;  // blocks of the range
 };
 
 struct KvPlan {  // views into the caller's plan buffer
     uint64_t* sig;       // [2]: of the rows (append), of rows and work (attention)
-    int64_t* total;      // W
     int64_t* prefix;     // [N + 1] blocks before each row
     KvStart* start;      // [G]
     KvCut* cut;          // [G]
@@ -53,6 +61,7 @@ struct KvPlan {  // views into the caller's plan buffer
 struct KvShape {  // what a plan is made for
     int S, N, n_global, max_len;
     int q_heads, kv_heads, nsub, r, G;
+    int cut;             // 0: units stay whole
     uint64_t sig_rows, sig_all;
     int32_t dil[kMaxHeads];
 };
@@ -79,7 +88,6 @@ inline KvPlan kv_plan_view(void* buf, const KvPlanLayout& L) {
     uint8_t* b = static_cast<uint8_t*>(buf);
     KvPlan p;
     p.sig = reinterpret_cast<uint64_t*>(b);
-    p.total = reinterpret_cast<int64_t*>(b + 16);
     p.prefix = reinterpret_cast<int64_t*>(b + L.prefix);
     p.start = reinterpret_cast<KvStart*>(b + L.start);
     p.cut = reinterpret_cast<KvCut*>(b + L.cut);
@@ -223,13 +231,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
     const int64_t W = s_carry;
     if (tid == 0) {
         p.prefix[sh.N] = W;
-        p.total[0] = W;
         p.sig[0] = sh.sig_rows;
         p.sig[1] = sh.sig_all;
     }
     __syncthreads();
     // The split.  Block x of the sequence: its row, unit, and place in the unit.
-    const int64_t G = W < sh.G ? W : sh.G;  // no CTA below G is without a block
+    const int64_t wide = (W + kKvMinBlocks - 1) / kKvMinBlocks;
+    const int64_t G = wide < sh.G ? wide : sh.G;  // no CTA below G has an empty range
     auto locate = [&](int64_t x, KvStart& at, int64_t& unit_first, int64_t& unit_end) {
         int lo = 0, hi = sh.N;  // the last row with prefix <= x (rows without blocks are passed over)
         while (hi - lo > 1) {
@@ -238,10 +246,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
             else hi = mid;
         }
         int64_t left = x - p.prefix[lo];
-        const int pos = p.row_pos[lo], ng = p.row_ng[lo];
+        at.row = lo;
+        at.seq = p.row_seq[lo];
+        at.pos = p.row_pos[lo];
+        at.ng = p.row_ng[lo];
         int unit = 0, nb = 1;
         for (int h = 0; h < sh.kv_heads; ++h) {
-            nb = KvKeys(pos, ng, sh.r, sh.dil[h]).blocks();
+            nb = KvKeys(at.pos, at.ng, sh.r, sh.dil[h]).blocks();
             const int64_t all = int64_t(nb) * sh.nsub;
             if (left < all) {
                 unit = h * sh.nsub + static_cast<int>(left / nb);
@@ -250,26 +261,40 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
             }
             left -= all;
         }
-        at.row = lo;
         at.unit = unit;
         at.blk = static_cast<int>(left);
-        at.pad = 0;
         unit_first = x - left;
         unit_end = unit_first + nb;
     };
-    for (int s = tid; s < sh.G; s += kPlanThreads) {
-        const int64_t x0 = s < G ? s * W / G : 0, x1 = s < G ? (s + 1) * W / G : 0;
-        KvStart at{0, 0, 0, 0};
-        KvCut cut{0, 0, -1, 0};
+    // the first unit boundary at or behind block x
+    auto boundary = [&](int64_t x) {
+        if (x >= W) return W;
+        KvStart at;
         int64_t first, end;
-        if (x0 < x1) {
-            locate(x0, at, first, end);
-            KvStart last;
-            locate(x1 - 1, last, first, end);
-            if (first >= x0 && end > x1) {
-                cut.row = last.row;
-                cut.unit = last.unit;
-                cut.last = static_cast<int>((end * G - 1) / W);  // the CTA that has block end - 1
+        locate(x, at, first, end);
+        return first == x ? x : end;
+    };
+    for (int s = tid; s < sh.G; s += kPlanThreads) {
+        KvStart at{0, 0, 0, 0, 0, 0, 0};
+        KvCut cut{0, 0, -1, 0};
+        if (s < G) {
+            int64_t x0 = s * W / G, x1 = (s + 1) * W / G, first, end;
+            if (!sh.cut) {
+                x0 = boundary(x0);
+                x1 = boundary(x1);
+            }
+            if (x0 < x1) {
+                locate(x0, at, first, end);
+                at.n = x1 - x0;
+                if (sh.cut) {
+                    KvStart last;
+                    locate(x1 - 1, last, first, end);
+                    if (first >= x0 && end > x1) {
+                        cut.row = last.row;
+                        cut.unit = last.unit;
+                        cut.last = static_cast<int>((end * G - 1) / W);  // the CTA that has block end - 1
+                    }
+                }
             }
         }
         p.start[s] = at;

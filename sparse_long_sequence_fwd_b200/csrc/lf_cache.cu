@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "lf_attn.h"
 #include "kv_append.cuh"
@@ -22,10 +23,10 @@ namespace {
 using namespace lf;
 
 constexpr double kLog2e = 1.4426950408889634;
-// The attention's CTAs: four per SM of a 148-SM B200 (larger GPUs run it on
-// as many), so plan and workspace have sizes known without a device.
-constexpr int kKvGrid = 148 * kKvCtasPerSm;
-static_assert(kKvGrid <= kKvMaxCtas, "");
+// The attention's CTAs: as many as a 148-SM B200 holds at once (larger GPUs run
+// it on as many), so plan and workspace have sizes known without a device.
+int kv_grid(int d, int bits, int gs) { return 148 * kv_ctas_per_sm(d, bits, gs > 8); }
+static_assert(148 * 4 <= kKvMaxCtas, "");
 constexpr int kMaxRotHeads = 1024;
 constexpr int kAppendSmem = 100 * 1024;
 constexpr int kAppendTileSmem = 40 * 1024;  // staged rows of a tile of more than one token
@@ -88,14 +89,17 @@ uint64_t mix(uint64_t h, uint64_t x) {  // FNV-1a over the value's bytes
     return h;
 }
 
-lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_heads, int kv_heads, int r,
-                   const int32_t* dil, KvShape* sh) {
+int heads_of_unit(int group, int nsub) { return (group + nsub - 1) / nsub; }
+
+lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_heads, int kv_heads, int d, int bits,
+                   int r, const int32_t* dil, KvShape* sh) {
     if (S < 1 || N < 0 || n_global < 0 || page < 1 || max_pages < 1 || q_heads < 1 || kv_heads < 1 || r < 0)
         return LF_ERR_INVALID_ARG;
-    if (q_heads % kv_heads != 0) return LF_ERR_INVALID_ARG;
+    if (q_heads % kv_heads != 0 || d < 1 || (bits != 16 && bits != 4)) return LF_ERR_INVALID_ARG;
     if (dil)
         for (int h = 0; h < kv_heads && h < kMaxHeads; ++h)
             if (dil[h] < 1) return LF_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return LF_ERR_UNSUPPORTED;
     if (page < 8 || page > 256 || (page & (page - 1)) != 0) return LF_ERR_UNSUPPORTED;
     if (q_heads > kMaxHeads || n_global > kKvMaxGlobal || S > (1 << 20) || N > (1 << 20)) return LF_ERR_UNSUPPORTED;
     if (int64_t(max_pages) * page > (int64_t(1) << 30)) return LF_ERR_UNSUPPORTED;
@@ -114,12 +118,14 @@ lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_he
     // no more CTAs than blocks that ordinary rows can have
     const int64_t keys = std::min<int64_t>(int64_t(sh->r) + 1, sh->max_len);
     const int64_t blocks = (keys + kKvBlock - 1) / kKvBlock + (n_global + kKvBlock - 1) / kKvBlock;
-    sh->G = static_cast<int>(
-        std::max<int64_t>(1, std::min<int64_t>(kKvGrid, blocks * std::min(N, kKvGrid) * kv_heads * sh->nsub)));
+    const int64_t grid = kv_grid(d, bits, heads_of_unit(group, sh->nsub));
+    sh->cut = blocks > kKvWholeBlocks;
+    sh->G = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>(grid, blocks * std::min<int64_t>(N, grid) * kv_heads * sh->nsub)));
     uint64_t h = 14695981039346656037ull;
     for (int64_t x : {int64_t(S), int64_t(N), int64_t(page), int64_t(max_pages)}) h = mix(h, uint64_t(x));
     sh->sig_rows = h;
-    for (int64_t x : {int64_t(n_global), int64_t(q_heads), int64_t(kv_heads), int64_t(sh->r)}) h = mix(h, uint64_t(x));
+    for (int64_t x : {int64_t(n_global), int64_t(q_heads), int64_t(kv_heads), int64_t(sh->r), int64_t(d), int64_t(bits)}) h = mix(h, uint64_t(x));
     for (int a = 0; a < kv_heads; ++a) h = mix(h, uint64_t(sh->dil[a]));
     sh->sig_all = h;
     return LF_OK;
@@ -132,14 +138,13 @@ int log2_of(int x) {
 }
 
 lf_status check_cache(const void* k, const void* v, const void* k_par, const void* v_par, int n_pages, int kv_heads,
-                      int page, int d, lf_dtype dtype, int bits) {
-    if (!k || !v || n_pages < 1 || d < 1) return LF_ERR_INVALID_ARG;
-    if (bits != 16 && bits != 4) return LF_ERR_INVALID_ARG;
+                      int page, lf_dtype dtype, int bits) {
+    if (!k || !v || n_pages < 1) return LF_ERR_INVALID_ARG;
     if ((bits == 4) != (k_par != nullptr) || (bits == 4) != (v_par != nullptr)) return LF_ERR_INVALID_ARG;
     for (const void* p : {k, v, k_par, v_par})
         if (!aligned(p, 16)) return LF_ERR_INVALID_ARG;
     if (!known(dtype)) return LF_ERR_INVALID_ARG;
-    if (dtype == LF_F32 || (d != 64 && d != 128)) return LF_ERR_UNSUPPORTED;
+    if (dtype == LF_F32) return LF_ERR_UNSUPPORTED;
     if (int64_t(n_pages) * kv_heads * page > INT32_MAX) return LF_ERR_UNSUPPORTED;
     return LF_OK;
 }
@@ -147,9 +152,37 @@ lf_status check_cache(const void* k, const void* v, const void* k_par, const voi
 using AttnKernel = void (*)(KvAttnParams);
 
 template <int HD, int kBits>
-AttnKernel attn_kernel(bool half, bool two) {
-    if (half) return two ? kv_attn_kernel<HD, kBits, true, 2> : kv_attn_kernel<HD, kBits, true, 1>;
-    return two ? kv_attn_kernel<HD, kBits, false, 2> : kv_attn_kernel<HD, kBits, false, 1>;
+AttnKernel attn_kernel(bool half, int gs, int* smem) {
+    *smem = kv_attn_smem<HD, kBits>(gs);
+    if (half) return gs > 8 ? kv_attn_kernel<HD, kBits, true, 2> : kv_attn_kernel<HD, kBits, true, 1>;
+    return gs > 8 ? kv_attn_kernel<HD, kBits, false, 2> : kv_attn_kernel<HD, kBits, false, 1>;
+}
+
+// Shared-memory limits of the kernels, once per device.
+lf_status kernel_limits() {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return LF_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[dev]) return LF_OK;
+    for (int half = 0; half < 2; ++half)
+        for (int gs : {8, 16}) {
+            int smem[4];
+            const AttnKernel kern[4] = {attn_kernel<64, 16>(half, gs, &smem[0]), attn_kernel<64, 4>(half, gs, &smem[1]),
+                                        attn_kernel<128, 16>(half, gs, &smem[2]), attn_kernel<128, 4>(half, gs, &smem[3])};
+            for (int a = 0; a < 4; ++a)
+                if (cudaFuncSetAttribute(kern[a], cudaFuncAttributeMaxDynamicSharedMemorySize, smem[a]) != cudaSuccess ||
+                    cudaFuncSetAttribute(kern[a], cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+                    return LF_ERR_CUDA;
+        }
+    for (auto kern : {kv_append_kernel<__half, 4, true>, kv_append_kernel<__half, 4, false>,
+                      kv_append_kernel<__nv_bfloat16, 4, true>, kv_append_kernel<__nv_bfloat16, 4, false>})
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem) != cudaSuccess)
+            return LF_ERR_CUDA;
+    done[dev] = true;
+    return LF_OK;
 }
 
 }  // namespace
@@ -225,12 +258,12 @@ uint64_t lf_attn_cache_plan_bytes(int n_seqs, int n_tokens, int n_global) {
 
 lf_status lf_attn_cache_plan(const int32_t* cu_tokens, const int32_t* context, int n_seqs, int n_tokens,
                              const int32_t* global_idx, int n_global, int page, int max_pages, int q_heads,
-                             int kv_heads, int r, const int32_t* dil, void* plan, void* stream) {
+                             int kv_heads, int d, int bits, int r, const int32_t* dil, void* plan, void* stream) {
     if (!cu_tokens || !context || !plan || (n_global > 0) != (global_idx != nullptr)) return LF_ERR_INVALID_ARG;
     if (!aligned(cu_tokens, 4) || !aligned(context, 4) || !aligned(global_idx, 4) || !aligned(plan, 256))
         return LF_ERR_INVALID_ARG;
     KvShape sh;
-    lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, r, dil, &sh);
+    lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, r, dil, &sh);
     if (st != LF_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint32_t* status = nullptr;
@@ -254,9 +287,9 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
         !aligned(plan, 256) || !std::isfinite(amplitude))
         return LF_ERR_INVALID_ARG;
     KvShape sh;
-    lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, 0, nullptr, &sh);
+    lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, 0, nullptr, &sh);
     if (st != LF_OK) return st;
-    if ((st = check_cache(k_cache, v_cache, k_par, v_par, n_pages, kv_heads, page, d, dtype, bits)) != LF_OK) return st;
+    if ((st = check_cache(k_cache, v_cache, k_par, v_par, n_pages, kv_heads, page, dtype, bits)) != LF_OK) return st;
     KvAppendParams p{};
     const void* x[3] = {k, v, q};
     void* y[3] = {k_held, v_held, q_out};
@@ -287,7 +320,7 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     if (n_tokens == 0) return LF_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms = 0;
-    if ((st = device_info(s, &p.status, &sms)) != LF_OK) return st;
+    if ((st = device_info(s, &p.status, &sms)) != LF_OK || (st = kernel_limits()) != LF_OK) return st;
     p.cache[0] = static_cast<uint8_t*>(k_cache);
     p.cache[1] = static_cast<uint8_t*>(v_cache);
     p.par[0] = static_cast<uint8_t*>(k_par);
@@ -316,17 +349,16 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     else
         kern = bits == 16 ? (vec ? kv_append_kernel<__nv_bfloat16, 16, true> : kv_append_kernel<__nv_bfloat16, 16, false>)
                           : (vec ? kv_append_kernel<__nv_bfloat16, 4, true> : kv_append_kernel<__nv_bfloat16, 4, false>);
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem) != cudaSuccess)
-        return LF_ERR_CUDA;
     kern<<<grid, kRotThreads, smem, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
 }
 
-uint64_t lf_attn_cache_workspace_bytes(int q_heads, int kv_heads, int d) {
-    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (d != 64 && d != 128) || q_heads > kMaxHeads) return 0;
-    const int group = q_heads / kv_heads, nsub = (group + 15) / 16, gs = (group + nsub - 1) / nsub;
-    return uint64_t(2) * kKvGrid * gs * (d + 2) * sizeof(float);
+uint64_t lf_attn_cache_workspace_bytes(int q_heads, int kv_heads, int d, int bits) {
+    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (d != 64 && d != 128) || q_heads > kMaxHeads ||
+        (bits != 16 && bits != 4))
+        return 0;
+    const int group = q_heads / kv_heads, gs = heads_of_unit(group, (group + 15) / 16);
+    return uint64_t(2) * kv_grid(d, bits, gs) * gs * kv_piece_row(d) * sizeof(float);
 }
 
 lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, const void* k_cache, const void* v_cache,
@@ -337,21 +369,21 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     if (!q || !out || !strides || !table || !plan || !workspace || !std::isfinite(scale)) return LF_ERR_INVALID_ARG;
     if (!aligned(table, 4) || !aligned(plan, 256) || !aligned(workspace, 16)) return LF_ERR_INVALID_ARG;
     KvShape sh;
-    lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, r, dil, &sh);
+    lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, r, dil, &sh);
     if (st != LF_OK) return st;
-    if ((st = check_cache(k_cache, v_cache, k_par, v_par, n_pages, kv_heads, page, d, dtype, bits)) != LF_OK) return st;
+    if ((st = check_cache(k_cache, v_cache, k_par, v_par, n_pages, kv_heads, page, dtype, bits)) != LF_OK) return st;
     const int64_t n[2] = {n_tokens, q_heads};
     Span a, b;
     if (!span_of(q, 2, n, strides, d, 2, &a) || !span_of(out, 2, n, strides + 2, d, 2, &b) ||
         !distinct(2, n, strides + 2) || !by_eight(q, 2, strides, 2) || !aligned(out, 2) || a.meets(b))
         return LF_ERR_INVALID_ARG;
-    if (workspace_bytes < lf_attn_cache_workspace_bytes(q_heads, kv_heads, d)) return LF_ERR_SCRATCH_TOO_SMALL;
+    if (workspace_bytes < lf_attn_cache_workspace_bytes(q_heads, kv_heads, d, bits)) return LF_ERR_SCRATCH_TOO_SMALL;
     if (n_tokens == 0) return LF_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     KvAttnParams p;
     std::memset(&p, 0, sizeof(p));
     int sms = 0;
-    if ((st = device_info(s, &p.status, &sms)) != LF_OK) return st;
+    if ((st = device_info(s, &p.status, &sms)) != LF_OK || (st = kernel_limits()) != LF_OK) return st;
     p.q = q;
     p.out = out;
     p.q_row = strides[0];
@@ -372,23 +404,25 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     p.kv_heads = kv_heads;
     p.group = q_heads / kv_heads;
     p.nsub = sh.nsub;
-    p.gs = (p.group + p.nsub - 1) / p.nsub;
+    p.gs = heads_of_unit(p.group, p.nsub);
     p.r = sh.r;
     p.n_global = n_global;
     p.G = sh.G;
     p.sl2 = static_cast<float>(double(scale) * kLog2e);
     p.sig = sh.sig_all;
     std::memcpy(p.dil, sh.dil, sizeof(p.dil));
-    const bool half = dtype == LF_F16, two = p.gs > 8;
-    const AttnKernel kern = d == 64 ? (bits == 16 ? attn_kernel<64, 16>(half, two) : attn_kernel<64, 4>(half, two))
-                                    : (bits == 16 ? attn_kernel<128, 16>(half, two) : attn_kernel<128, 4>(half, two));
-    kern<<<p.G, kKvThreads, 0, s>>>(p);
+    const bool half = dtype == LF_F16;
+    int smem = 0;
+    const AttnKernel kern = d == 64 ? (bits == 16 ? attn_kernel<64, 16>(half, p.gs, &smem) : attn_kernel<64, 4>(half, p.gs, &smem))
+                                    : (bits == 16 ? attn_kernel<128, 16>(half, p.gs, &smem) : attn_kernel<128, 4>(half, p.gs, &smem));
+    kern<<<p.G, kKvThreads, smem, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return LF_ERR_CUDA;
+    if (!sh.cut) return LF_OK;
     const AttnKernel merge = d == 64 ? (half ? kv_merge_kernel<64, true> : kv_merge_kernel<64, false>)
                                      : (half ? kv_merge_kernel<128, true> : kv_merge_kernel<128, false>);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.G);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(p.G, p.gs);
+    cfg.blockDim = dim3(d);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -18,8 +18,11 @@ from typing import Optional
 import torch
 
 from . import lf_attn
-from .lf_attn import LfAttnError, _dil_array, _dtype_code, _ptr
-from .rotary import _check_freqs, _on
+from .lf_attn import LF_BF16, LF_F16, LfAttnError, _dil_array, _ptr
+from .rotary import _check_freqs, _on_stream
+
+_I4, _I12 = ctypes.c_int64 * 4, ctypes.c_int64 * 12
+_CODES = {torch.bfloat16: LF_BF16, torch.float16: LF_F16}
 
 
 def _int32(t: torch.Tensor, shape, what: str) -> torch.Tensor:
@@ -68,9 +71,6 @@ class KVCache:
         par = [torch.empty(pages, kv_heads, page, d // 32, 2, dtype=torch.float16, device=device) for _ in range(2)]
         return cls(*codes, *par)
 
-    def tensors(self):
-        return [t for t in (self.k, self.v, self.k_par, self.v_par) if t is not None]
-
 
 class Plan:
     """One step over caches shaped as ``cache``: rows [cu_tokens[s], cu_tokens[s+1]) of the step's n_tokens rows are
@@ -98,9 +98,11 @@ class Plan:
         size = lf_attn.load().lf_attn_cache_plan_bytes(S, self.n_tokens, self.n_global)
         if size == 0:
             raise LfAttnError(1, "lf_attn_cache_plan_bytes")
-        stack, _ = _on(stream, self._inputs())
-        with stack:
-            self.buffer = torch.empty(size, dtype=torch.uint8, device=context.device)
+        self.d, self.bits = cache.d, cache.bits
+        self.workspace_bytes = lf_attn.load().lf_attn_cache_workspace_bytes(self.q_heads, self.kv_heads, self.d,
+                                                                               self.bits)
+        self.buffer = _on_stream(stream, self._inputs(),
+                                 lambda raw: torch.empty(size, dtype=torch.uint8, device=context.device))
         self.refresh(stream)
 
     def _inputs(self):
@@ -108,29 +110,47 @@ class Plan:
 
     def refresh(self, stream: Optional[torch.cuda.Stream] = None) -> "Plan":
         """Lays the step out again, from what cu_tokens, context and global_idx hold when the call runs."""
-        stack, s = _on(stream, self._inputs() + [self.buffer])
-        with stack:
+        def call(raw):
             st = lf_attn.load().lf_attn_cache_plan(
                 _ptr(self.cu_tokens), _ptr(self.context), self.n_seqs, self.n_tokens, _ptr(self.global_idx),
-                self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.r, self.dil,
-                _ptr(self.buffer), s)
-        if st != 0:
-            raise LfAttnError(st, "lf_attn_cache_plan")
+                self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.d, self.bits,
+                self.r, self.dil,
+                _ptr(self.buffer), raw)
+            if st != 0:
+                raise LfAttnError(st, "lf_attn_cache_plan")
+
+        _on_stream(stream, self._inputs() + [self.buffer], call)
         return self
 
     def _check(self, cache: KVCache):
-        if (cache.kv_heads, cache.page) != (self.kv_heads, self.page):
-            raise ValueError("the plan was made for a cache with other heads or pages")
+        if cache.kv_heads != self.kv_heads or cache.page != self.page or cache.d != self.d or \
+                cache.bits != self.bits:
+            raise ValueError("the plan was made for a cache with other heads, pages or bits")
 
 
-def _rows(t: torch.Tensor, plan: Plan, heads: int, d: int, dtype, what: str) -> torch.Tensor:
-    if tuple(t.shape) != (plan.n_tokens, heads, d):
-        raise ValueError("%s must be [n_tokens, heads, d] = %s" % (what, [plan.n_tokens, heads, d]))
+def _rows(t: torch.Tensor, n: int, heads: int, d: int, dtype, what: str):
+    """The (token, head) strides of rows t, checked."""
+    if t.shape != (n, heads, d):
+        raise ValueError("%s must be [n_tokens, heads, d] = %s" % (what, [n, heads, d]))
     if t.dtype != dtype:
         raise TypeError("%s must be %s" % (what, dtype))
-    if t.stride(2) != 1:
+    a, b, c = t.stride()
+    if c != 1:
         raise ValueError("the d values of a row of %s must be contiguous" % what)
-    return t
+    return a, b
+
+
+def _code(cache: KVCache, dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError("rows must be bfloat16 or float16, got %s" % dtype)
+    if cache.bits == 16 and dtype != cache.k.dtype:
+        raise TypeError("rows and cache must share a dtype")
+    return code
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -142,45 +162,44 @@ def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Opti
     ``held`` asks for what the cache now holds of these rows, as dense 16-bit rows (for 4 bits the dequantised
     values): True for new tensors, or the two to write; append then gives (q, k_held, v_held)."""
     plan._check(cache)
-    dtype = k.dtype
-    code = _dtype_code(k)
-    if cache.bits == 16 and dtype != cache.k.dtype:
-        raise TypeError("rows and cache must share a dtype")
-    _rows(k, plan, cache.kv_heads, cache.d, dtype, "k")
-    _rows(v, plan, cache.kv_heads, cache.d, dtype, "v")
-    if q is not None:
-        _rows(q, plan, plan.q_heads, cache.d, dtype, "q")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
+    dtype, n, hkv, d = k.dtype, plan.n_tokens, cache.kv_heads, cache.d
+    code = _code(cache, dtype)
+    strides = [*_rows(k, n, hkv, d, dtype, "k"), *_rows(v, n, hkv, d, dtype, "v"),
+               *(_rows(q, n, plan.q_heads, d, dtype, "q") if q is not None else (0, 0))]
     if q_out is not None:
-        _rows(q_out, plan, plan.q_heads, cache.d, dtype, "q_out")
-    given = held is not None and held is not False and held is not True
-    if given:
-        for t in held:
-            _rows(t, plan, cache.kv_heads, cache.d, dtype, "held")
+        if q is None:
+            raise ValueError("q_out without q")
+        _rows(q_out, n, plan.q_heads, d, dtype, "q_out")
+    hk = hv = None
+    if held is not None and held is not False and held is not True:
         if len(held) != 2:
             raise ValueError("held must be True or the two tensors to write")
-    rot = _check_freqs(freqs, cache.d)
-    used = [k, v, plan.buffer, plan.table] + cache.tensors() + [t for t in (q, freqs, q_out) if t is not None]
-    stack, s = _on(stream, used + (list(held) if given else []))
-    with stack:
+        hk, hv = held
+        for t in held:
+            _rows(t, n, hkv, d, dtype, "held")
+    rot = _check_freqs(freqs, d)
+    used = [t for t in (k, v, plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par, q, freqs, q_out, hk,
+                        hv) if t is not None]
+
+    def call(raw):
+        nonlocal q_out, hk, hv
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
         if held is True:
-            held = [torch.empty(k.shape, dtype=dtype, device=k.device) for _ in range(2)]
-        hk, hv = held if held is not None and held is not False else (None, None)
-        if plan.n_tokens == 0:  # empty tensors have no address
-            return (q_out, hk, hv) if hk is not None else q_out
-        strides = (ctypes.c_int64 * 12)(*[0 if t is None else t.stride(i) for t in (k, v, q, hk, hv, q_out)
-                                          for i in range(2)])
-        st = lf_attn.load().lf_attn_cache_append(
-            _ptr(k), _ptr(v), _ptr(q), _ptr(hk), _ptr(hv), _ptr(q_out), strides, _ptr(cache.k), _ptr(cache.v),
-            _ptr(cache.k_par), _ptr(cache.v_par), cache.pages, cache.page, _ptr(plan.table), plan.max_pages,
-            _ptr(plan.buffer), plan.n_seqs, plan.n_tokens, plan.n_global, plan.q_heads, cache.kv_heads, cache.d,
-            _ptr(freqs) if rot else None, rot, 1 if interleaved else 0, float(amplitude), code, cache.bits, s)
-    if st != 0:
-        raise LfAttnError(st, "lf_attn_cache_append")
-    return (q_out, hk, hv) if hk is not None else q_out
+            hk, hv = (torch.empty(k.shape, dtype=dtype, device=k.device) for _ in range(2))
+        if n > 0:  # empty tensors have no address
+            for t in (hk, hv, q_out):
+                strides.extend((0, 0) if t is None else t.stride()[:2])
+            st = lf_attn.load().lf_attn_cache_append(
+                k.data_ptr(), v.data_ptr(), _at(q), _at(hk), _at(hv), _at(q_out), _I12(*strides), cache.k.data_ptr(),
+                cache.v.data_ptr(), _at(cache.k_par), _at(cache.v_par), cache.pages, cache.page, plan.table.data_ptr(),
+                plan.max_pages, plan.buffer.data_ptr(), plan.n_seqs, n, plan.n_global, plan.q_heads, hkv, d,
+                freqs.data_ptr() if rot else None, rot, 1 if interleaved else 0, amplitude, code, cache.bits, raw)
+            if st != 0:
+                raise LfAttnError(st, "lf_attn_cache_append")
+        return (q_out, hk, hv) if hk is not None else q_out
+
+    return _on_stream(stream, used, call)
 
 
 def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = None,
@@ -188,35 +207,30 @@ def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = No
         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The attention of the step's rows q [n_tokens, q_heads, d] over the cache, which already holds their own keys.
     Rows behind the last sequence are left as they are in ``out``.  ``workspace``: a uint8 tensor of
-    lf_attn_cache_workspace_bytes for callers that keep one (per stream)."""
+    ``plan.workspace_bytes`` for callers that keep one (per stream)."""
     plan._check(cache)
-    code = _dtype_code(q)
-    if cache.bits == 16 and q.dtype != cache.k.dtype:
-        raise TypeError("q and cache must share a dtype")
-    _rows(q, plan, plan.q_heads, cache.d, q.dtype, "q")
+    n, heads, d, dtype = plan.n_tokens, plan.q_heads, cache.d, q.dtype
+    code = _code(cache, dtype)
+    qs = _rows(q, n, heads, d, dtype, "q")
+    used = [t for t in (q, plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par, out, workspace)
+            if t is not None]
     if out is not None:
-        _rows(out, plan, plan.q_heads, cache.d, q.dtype, "out")
-    if scale is None:
-        scale = cache.d ** -0.5
-    lib = lf_attn.load()
+        _rows(out, n, heads, d, dtype, "out")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    used = [q, plan.buffer, plan.table] + cache.tensors() + [t for t in (out, workspace) if t is not None]
-    stack, s = _on(stream, used)
-    with stack:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if workspace is None:
-            size = lib.lf_attn_cache_workspace_bytes(plan.q_heads, cache.kv_heads, cache.d)
-            workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=q.device)
-        if plan.n_tokens == 0:
-            return out
-        strides = (ctypes.c_int64 * 4)(q.stride(0), q.stride(1), out.stride(0), out.stride(1))
-        st = lib.lf_attn_cache_fwd(
-            _ptr(q), _ptr(out), strides, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_par), _ptr(cache.v_par),
-            cache.pages, cache.page, _ptr(plan.table), plan.max_pages, _ptr(plan.buffer), plan.n_seqs, plan.n_tokens,
-            plan.n_global, plan.q_heads, cache.kv_heads, cache.d, plan.r, plan.dil, float(scale), code, cache.bits,
-            _ptr(workspace), workspace.numel(), s)
-    if st != 0:
-        raise LfAttnError(st, "lf_attn_cache_fwd")
-    return out
+
+    def call(raw):
+        y = torch.empty(q.shape, dtype=dtype, device=q.device) if out is None else out
+        if n == 0:  # empty tensors have no address
+            return y
+        ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device) if workspace is None else workspace
+        st = lf_attn.load().lf_attn_cache_fwd(
+            q.data_ptr(), y.data_ptr(), _I4(*qs, *y.stride()[:2]), cache.k.data_ptr(), cache.v.data_ptr(),
+            _at(cache.k_par), _at(cache.v_par), cache.pages, cache.page, plan.table.data_ptr(), plan.max_pages,
+            plan.buffer.data_ptr(), plan.n_seqs, n, plan.n_global, heads, cache.kv_heads, d, plan.r, plan.dil,
+            d ** -0.5 if scale is None else scale, code, cache.bits, ws.data_ptr(), ws.numel(), raw)
+        if st != 0:
+            raise LfAttnError(st, "lf_attn_cache_fwd")
+        return y
+
+    return _on_stream(stream, used, call)

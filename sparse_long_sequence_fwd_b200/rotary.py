@@ -7,7 +7,6 @@ of a packed gradient where ``out`` names them.  Work runs in the library's kerne
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import Optional, Sequence
@@ -15,7 +14,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import lf_attn
-from .lf_attn import LfAttnError, _dtype_code, _ptr
+from .lf_attn import LfAttnError
 
 
 def freqs(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -55,25 +54,33 @@ def freqs(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor
     return torch.tensor(f, dtype=torch.float64, device=device)
 
 
-def _on(stream: Optional[torch.cuda.Stream], tensors):
-    """The tensors' device, and ``stream`` (default: the device's current one) as the current stream: what is
-    allocated within belongs to that stream, and tensors of another one are marked as used by it."""
-    device = tensors[0].device
-    if device.type != "cuda":
+_I18 = ctypes.c_int64 * 18
+_CODES = {torch.float32: lf_attn.LF_F32, torch.bfloat16: lf_attn.LF_BF16, torch.float16: lf_attn.LF_F16}
+
+
+def _on_stream(stream: Optional[torch.cuda.Stream], tensors, call):
+    """call(raw stream) with ``stream`` (default: the device's current one) as the current stream of the tensors'
+    device: what the call allocates belongs to that stream, and tensors are marked as used by a stream that is not
+    the current one."""
+    index = tensors[0].get_device()
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if any(t.device != device for t in tensors):
-        raise ValueError("all tensors must be on one device")
-    stack = contextlib.ExitStack()
-    stack.enter_context(torch.cuda.device(device))
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("the stream is of another device than the tensors")
-        if stream != torch.cuda.current_stream(device):
-            if not torch.cuda.is_current_stream_capturing():
-                for t in tensors:
-                    t.record_stream(stream)
-            stack.enter_context(torch.cuda.stream(stream))
-    return stack, ctypes.c_void_p((stream or torch.cuda.current_stream(device)).cuda_stream)
+    for t in tensors:
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on one device")
+    if stream is None:
+        if torch.cuda.current_device() == index:
+            return call(torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            return call(torch._C._cuda_getCurrentRawStream(index))
+    if stream.device.index != index:
+        raise ValueError("the stream is of another device than the tensors")
+    with torch.cuda.device(index):
+        if stream != torch.cuda.current_stream() and not torch.cuda.is_current_stream_capturing():
+            for t in tensors:
+                t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _check_freqs(f: Optional[torch.Tensor], d: int) -> int:
@@ -81,62 +88,93 @@ def _check_freqs(f: Optional[torch.Tensor], d: int) -> int:
         return 0
     if f.dtype != torch.float64 or f.dim() != 1 or not f.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 [rot / 2] tensor")
-    if 2 * f.numel() > d:
+    rot = 2 * f.shape[0]
+    if rot > d:
         raise ValueError("rot = 2 * len(freqs) must not exceed the head dimension")
-    return 2 * f.numel()
+    return rot
 
 
 def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inverse):
-    rows = [q, k, v]
+    rows = (q, k, v)
     have = [t for t in rows if t is not None]
     if not have:
         raise ValueError("one of q, k and v must be given")
     first = have[0]
-    if any(t.dim() != 4 for t in have):
+    if first.dim() != 4:
         raise ValueError("q, k, v must be [B, heads, T, d]")
     B, _, T, d = first.shape
-    if any((t.shape[0], t.shape[2], t.shape[3]) != (B, T, d) for t in have):
-        raise ValueError("q, k, v must share B, T and d")
-    if k is not None and v is not None and k.shape[1] != v.shape[1]:
+    dtype = first.dtype
+    in_code = _CODES.get(dtype)
+    if in_code is None:
+        raise TypeError("q, k, v must be float32, bfloat16 or float16, got %s" % dtype)
+    heads = [0, 0, 0]
+    strides = []
+    for i, t in enumerate(rows):
+        if t is None:
+            strides += (0, 0, 0)
+            continue
+        if t.dim() != 4:
+            raise ValueError("q, k, v must be [B, heads, T, d]")
+        b, heads[i], n, e = t.shape
+        if b != B or n != T or e != d:
+            raise ValueError("q, k, v must share B, T and d")
+        if t.dtype != dtype:
+            raise TypeError("q, k, v must share a dtype")
+        sb, sh, sn, se = t.stride()
+        if se != 1 and e > 1:
+            raise ValueError("the d values of a row must be contiguous")
+        strides += (sb, sh, sn)
+    if k is not None and v is not None and heads[1] != heads[2]:
         raise ValueError("k and v must have the same heads")
-    if any(t.dtype != first.dtype for t in have):
-        raise TypeError("q, k, v must share a dtype")
     rot = _check_freqs(f, d)
-    if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) not in ((T,), (B, T)) or
-                            (T > 1 and pos.stride(-1) != 1)):
-        raise ValueError("pos must be an int32 [T] or [B, T] tensor with its last dimension contiguous")
+    pos_stride = 0
+    if pos is not None:
+        shape = tuple(pos.shape)
+        if pos.dtype != torch.int32 or (shape != (T,) and shape != (B, T)) or (T > 1 and pos.stride(-1) != 1):
+            raise ValueError("pos must be an int32 [T] or [B, T] tensor with its last dimension contiguous")
+        have.append(pos)
+        if len(shape) == 2:
+            pos_stride = pos.stride(0)
     if out is not None:
-        out = list(out)
+        out = tuple(out)
         if len(out) != 3:
             raise ValueError("out must name three tensors (None for absent ones)")
         for t, o in zip(rows, out):
             if (t is None) != (o is None) or (t is not None and o.shape != t.shape):
                 raise ValueError("out must have the shapes of q, k, v")
-        od = [o.dtype for o in out if o is not None]
-        if any(x != od[0] for x in od) or (out_dtype is not None and out_dtype != od[0]):
-            raise TypeError("out must share one dtype")
-        out_dtype = od[0]
-    out_dtype = out_dtype or first.dtype
-    codes = _dtype_code(first), _dtype_code(torch.empty(0, dtype=out_dtype))
-    for t in have + [o for o in out or [] if o is not None]:
-        if t.shape[3] > 1 and t.stride(3) != 1:
-            raise ValueError("the d values of a row must be contiguous")
-    used = have + [t for t in (f, pos) if t is not None] + [o for o in out or [] if o is not None]
-    stack, s = _on(stream, used)
-    with stack:
-        if out is None:
-            out = [None if t is None else torch.empty(t.shape, dtype=out_dtype, device=t.device) for t in rows]
-        if all(t.numel() == 0 for t in have):  # nothing to turn: empty tensors have no address
-            return tuple(out)
-        strides = (ctypes.c_int64 * 18)(*[0 if t is None else t.stride(i) for t in rows + out for i in range(3)])
+            if o is not None:
+                if out_dtype is None:
+                    out_dtype = o.dtype
+                if o.dtype != out_dtype:
+                    raise TypeError("out must share one dtype")
+                if o.shape[3] > 1 and o.stride(3) != 1:
+                    raise ValueError("the d values of a row must be contiguous")
+                have.append(o)
+    if out_dtype is None:
+        out_dtype = dtype
+    out_code = _CODES.get(out_dtype)
+    if out_code is None:
+        raise TypeError("out must be float32, bfloat16 or float16, got %s" % out_dtype)
+    if f is not None:
+        have.append(f)
+
+    def call(raw):
+        y = out
+        if y is None:
+            y = tuple([None if t is None else torch.empty(t.shape, dtype=out_dtype, device=t.device) for t in rows])
+        if B == 0 or T == 0 or not any(heads):  # nothing to turn: empty tensors have no address
+            return y
+        for t in y:
+            strides.extend((0, 0, 0) if t is None else t.stride()[:3])
         st = lf_attn.load().lf_attn_rotary(
-            *[_ptr(t) for t in rows + out], strides, B, q.shape[1] if q is not None else 0,
-            next((t.shape[1] for t in (k, v) if t is not None), 0), T, d, _ptr(pos),
-            pos.stride(0) if pos is not None and pos.dim() == 2 else 0, _ptr(f) if rot else None, rot,
-            1 if interleaved else 0, 1 if inverse else 0, float(amplitude), codes[0], codes[1], s)
-    if st != 0:
-        raise LfAttnError(st, "lf_attn_rotary")
-    return tuple(out)
+            *[None if t is None else t.data_ptr() for t in rows + y], _I18(*strides), B, heads[0],
+            heads[1] or heads[2], T, d, None if pos is None else pos.data_ptr(), pos_stride,
+            f.data_ptr() if rot else None, rot, 1 if interleaved else 0, inverse, amplitude, in_code, out_code, raw)
+        if st != 0:
+            raise LfAttnError(st, "lf_attn_rotary")
+        return y
+
+    return _on_stream(stream, have, call)
 
 
 def fwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, *,
@@ -146,7 +184,7 @@ def fwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None, v: Optional
     """(q, k, v) with q and k turned by their positions and v copied, each [B, heads, T, d] and contiguous unless
     ``out`` gives the three tensors to write.  ``pos``: int32 [T] or [B, T] (default 0 .. T-1).  Pairs are
     (i, i + rot / 2), or (2i, 2i + 1) when ``interleaved``.  ``out_dtype`` may be a 16-bit type for fp32 rows."""
-    return _turn(q, k, v, freqs, pos, interleaved, amplitude, out, out_dtype, stream, False)
+    return _turn(q, k, v, freqs, pos, interleaved, amplitude, out, out_dtype, stream, 0)
 
 
 def bwd(dq: Optional[torch.Tensor], dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None, *,
@@ -155,4 +193,4 @@ def bwd(dq: Optional[torch.Tensor], dk: Optional[torch.Tensor] = None, dv: Optio
         stream: Optional[torch.cuda.Stream] = None):
     """The gradients of fwd's q, k, v from those of its outputs (the transpose: turned by the negative angle), for
     instance lf_attn.bwd's fp32 ones into the 16-bit views ``out`` of a packed gradient."""
-    return _turn(dq, dk, dv, freqs, pos, interleaved, amplitude, out, out_dtype, stream, True)
+    return _turn(dq, dk, dv, freqs, pos, interleaved, amplitude, out, out_dtype, stream, 1)

@@ -56,16 +56,17 @@ def test_rotary_refusals(lib, kw, code):
     assert call(lib.lf_attn_rotary, ROTARY, ROTARY_ORDER, **kw) == code
 
 
-PLAN = dict(cu=FAKE, ctx=FAKE, S=2, N=2, g=None, ng=0, page=16, mp=8, hq=4, hkv=2, r=5, dil=None, plan=FAKE, stream=None,
+PLAN = dict(cu=FAKE, ctx=FAKE, S=2, N=2, g=None, ng=0, page=16, mp=8, hq=4, hkv=2, d=64, bits=16, r=5, dil=None, plan=FAKE, stream=None,
             _p=("cu", "ctx", "g", "plan"))
-PLAN_ORDER = "cu ctx S N g ng page mp hq hkv r dil plan stream".split()
+PLAN_ORDER = "cu ctx S N g ng page mp hq hkv d bits r dil plan stream".split()
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(cu=None), INVALID), (dict(ctx=None), INVALID), (dict(plan=None), INVALID), (dict(plan=FAKE + 128), INVALID),
     (dict(ng=2), INVALID), (dict(g=FAKE), INVALID), (dict(ng=-1), INVALID), (dict(S=0), INVALID), (dict(N=-1), INVALID),
     (dict(page=0), INVALID), (dict(mp=0), INVALID), (dict(hq=3), INVALID), (dict(hkv=0), INVALID), (dict(r=-1), INVALID),
-    (dict(dil=i32(1, 0)), INVALID), (dict(cu=FAKE + 2), INVALID),
+    (dict(dil=i32(1, 0)), INVALID), (dict(cu=FAKE + 2), INVALID), (dict(bits=8), INVALID), (dict(d=0), INVALID),
+    (dict(d=96), UNSUPPORTED),
     (dict(page=4), UNSUPPORTED), (dict(page=48), UNSUPPORTED), (dict(page=512), UNSUPPORTED), (dict(hq=256), UNSUPPORTED),
     (dict(g=FAKE, ng=1025), UNSUPPORTED), (dict(mp=1 << 27), UNSUPPORTED), (dict(N=(1 << 20) + 1), UNSUPPORTED),
     (dict(S=(1 << 20) + 1), UNSUPPORTED),
@@ -78,8 +79,8 @@ def test_sizes(lib):
     assert lib.lf_attn_cache_plan_bytes(1, 0, 0) > 0
     for bad in ((0, 1, 0), (1, -1, 0), (1, 1, -1), (1, 1, 1025), ((1 << 20) + 1, 1, 0)):
         assert lib.lf_attn_cache_plan_bytes(*bad) == 0
-    assert lib.lf_attn_cache_workspace_bytes(12, 12, 64) > 0
-    for bad in ((12, 5, 64), (0, 1, 64), (12, 12, 96), (256, 1, 64)):
+    assert lib.lf_attn_cache_workspace_bytes(12, 12, 64, 16) > 0
+    for bad in ((12, 5, 64, 16), (0, 1, 64, 16), (12, 12, 96, 16), (256, 1, 64, 4), (12, 12, 64, 8)):
         assert lib.lf_attn_cache_workspace_bytes(*bad) == 0
 
 
