@@ -353,11 +353,12 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
 }
 
-uint64_t lf_attn_cache_workspace_bytes(int q_heads, int kv_heads, int d, int bits) {
-    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (d != 64 && d != 128) || q_heads > kMaxHeads ||
-        (bits != 16 && bits != 4))
+uint64_t lf_attn_cache_workspace_bytes(int n_global, int page, int max_pages, int q_heads, int kv_heads, int d,
+                                       int bits, int r) {
+    KvShape sh;
+    if (kv_shape(1, 1, n_global, page, max_pages, q_heads, kv_heads, d, bits, r, nullptr, &sh) != LF_OK || !sh.cut)
         return 0;
-    const int group = q_heads / kv_heads, gs = heads_of_unit(group, (group + 15) / 16);
+    const int gs = heads_of_unit(q_heads / kv_heads, sh.nsub);
     return uint64_t(2) * kv_grid(d, bits, gs) * gs * kv_piece_row(d) * sizeof(float);
 }
 
@@ -366,7 +367,7 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
                             int max_pages, const void* plan, int n_seqs, int n_tokens, int n_global, int q_heads,
                             int kv_heads, int d, int r, const int32_t* dil, float scale, lf_dtype dtype, int bits,
                             void* workspace, uint64_t workspace_bytes, void* stream) {
-    if (!q || !out || !strides || !table || !plan || !workspace || !std::isfinite(scale)) return LF_ERR_INVALID_ARG;
+    if (!q || !out || !strides || !table || !plan || !std::isfinite(scale)) return LF_ERR_INVALID_ARG;
     if (!aligned(table, 4) || !aligned(plan, 256) || !aligned(workspace, 16)) return LF_ERR_INVALID_ARG;
     KvShape sh;
     lf_status st = kv_shape(n_seqs, n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, r, dil, &sh);
@@ -377,7 +378,9 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     if (!span_of(q, 2, n, strides, d, 2, &a) || !span_of(out, 2, n, strides + 2, d, 2, &b) ||
         !distinct(2, n, strides + 2) || !by_eight(q, 2, strides, 2) || !aligned(out, 2) || a.meets(b))
         return LF_ERR_INVALID_ARG;
-    if (workspace_bytes < lf_attn_cache_workspace_bytes(q_heads, kv_heads, d, bits)) return LF_ERR_SCRATCH_TOO_SMALL;
+    const uint64_t need = lf_attn_cache_workspace_bytes(n_global, page, max_pages, q_heads, kv_heads, d, bits, r);
+    if (need > 0 && !workspace) return LF_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return LF_ERR_SCRATCH_TOO_SMALL;
     if (n_tokens == 0) return LF_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     KvAttnParams p;

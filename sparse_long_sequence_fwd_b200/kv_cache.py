@@ -12,7 +12,7 @@ kernels only.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -21,7 +21,7 @@ from . import lf_attn
 from .lf_attn import LF_BF16, LF_F16, LfAttnError, _dil_array, _ptr
 from .rotary import _check_freqs, _on_stream
 
-_I4, _I12 = ctypes.c_int64 * 4, ctypes.c_int64 * 12
+_PACK4, _PACK12 = struct.Struct("4q").pack, struct.Struct("12q").pack
 _CODES = {torch.bfloat16: LF_BF16, torch.float16: LF_F16}
 
 
@@ -99,8 +99,8 @@ class Plan:
         if size == 0:
             raise LfAttnError(1, "lf_attn_cache_plan_bytes")
         self.d, self.bits = cache.d, cache.bits
-        self.workspace_bytes = lf_attn.load().lf_attn_cache_workspace_bytes(self.q_heads, self.kv_heads, self.d,
-                                                                               self.bits)
+        self.workspace_bytes = lf_attn.load().lf_attn_cache_workspace_bytes(
+            self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.d, self.bits, self.r)
         self.buffer = _on_stream(stream, self._inputs(),
                                  lambda raw: torch.empty(size, dtype=torch.uint8, device=context.device))
         self.refresh(stream)
@@ -132,7 +132,7 @@ def _rows(t: torch.Tensor, n: int, heads: int, d: int, dtype, what: str):
     """The (token, head) strides of rows t, checked."""
     if t.shape != (n, heads, d):
         raise ValueError("%s must be [n_tokens, heads, d] = %s" % (what, [n, heads, d]))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s" % (what, dtype))
     a, b, c = t.stride()
     if c != 1:
@@ -183,15 +183,16 @@ def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Opti
 
     def call(raw):
         nonlocal q_out, hk, hv
+        new = lambda t: torch.empty_like(t, memory_format=torch.contiguous_format)  # noqa: E731
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            q_out = new(q)
         if held is True:
-            hk, hv = (torch.empty(k.shape, dtype=dtype, device=k.device) for _ in range(2))
+            hk, hv = new(k), new(v)
         if n > 0:  # empty tensors have no address
             for t in (hk, hv, q_out):
                 strides.extend((0, 0) if t is None else t.stride()[:2])
             st = lf_attn.load().lf_attn_cache_append(
-                k.data_ptr(), v.data_ptr(), _at(q), _at(hk), _at(hv), _at(q_out), _I12(*strides), cache.k.data_ptr(),
+                k.data_ptr(), v.data_ptr(), _at(q), _at(hk), _at(hv), _at(q_out), _PACK12(*strides), cache.k.data_ptr(),
                 cache.v.data_ptr(), _at(cache.k_par), _at(cache.v_par), cache.pages, cache.page, plan.table.data_ptr(),
                 plan.max_pages, plan.buffer.data_ptr(), plan.n_seqs, n, plan.n_global, plan.q_heads, hkv, d,
                 freqs.data_ptr() if rot else None, rot, 1 if interleaved else 0, amplitude, code, cache.bits, raw)
@@ -207,7 +208,7 @@ def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = No
         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The attention of the step's rows q [n_tokens, q_heads, d] over the cache, which already holds their own keys.
     Rows behind the last sequence are left as they are in ``out``.  ``workspace``: a uint8 tensor of
-    ``plan.workspace_bytes`` for callers that keep one (per stream)."""
+    ``plan.workspace_bytes`` (0: none is needed) for callers that keep one per stream."""
     plan._check(cache)
     n, heads, d, dtype = plan.n_tokens, plan.q_heads, cache.d, q.dtype
     code = _code(cache, dtype)
@@ -220,15 +221,17 @@ def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = No
         raise ValueError("workspace must be a contiguous uint8 tensor")
 
     def call(raw):
-        y = torch.empty(q.shape, dtype=dtype, device=q.device) if out is None else out
+        y = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
         if n == 0:  # empty tensors have no address
             return y
-        ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device) if workspace is None else workspace
+        ws = workspace
+        if ws is None and plan.workspace_bytes:
+            ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
         st = lf_attn.load().lf_attn_cache_fwd(
-            q.data_ptr(), y.data_ptr(), _I4(*qs, *y.stride()[:2]), cache.k.data_ptr(), cache.v.data_ptr(),
+            q.data_ptr(), y.data_ptr(), _PACK4(*qs, *y.stride()[:2]), cache.k.data_ptr(), cache.v.data_ptr(),
             _at(cache.k_par), _at(cache.v_par), cache.pages, cache.page, plan.table.data_ptr(), plan.max_pages,
             plan.buffer.data_ptr(), plan.n_seqs, n, plan.n_global, heads, cache.kv_heads, d, plan.r, plan.dil,
-            d ** -0.5 if scale is None else scale, code, cache.bits, ws.data_ptr(), ws.numel(), raw)
+            d ** -0.5 if scale is None else scale, code, cache.bits, _at(ws), 0 if ws is None else ws.numel(), raw)
         if st != 0:
             raise LfAttnError(st, "lf_attn_cache_fwd")
         return y

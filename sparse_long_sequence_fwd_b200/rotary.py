@@ -7,8 +7,8 @@ of a packed gradient where ``out`` names them.  Work runs in the library's kerne
 """
 from __future__ import annotations
 
-import ctypes
 import math
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -54,8 +54,9 @@ def freqs(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor
     return torch.tensor(f, dtype=torch.float64, device=device)
 
 
-_I18 = ctypes.c_int64 * 18
+_PACK18 = struct.Struct("18q").pack
 _CODES = {torch.float32: lf_attn.LF_F32, torch.bfloat16: lf_attn.LF_BF16, torch.float16: lf_attn.LF_F16}
+_NONE = (0, 0, 0)
 
 
 def _on_stream(stream: Optional[torch.cuda.Stream], tensors, call):
@@ -86,20 +87,18 @@ def _on_stream(stream: Optional[torch.cuda.Stream], tensors, call):
 def _check_freqs(f: Optional[torch.Tensor], d: int) -> int:
     if f is None:
         return 0
-    if f.dtype != torch.float64 or f.dim() != 1 or not f.is_contiguous():
+    if f.dtype is not torch.float64 or f.dim() != 1 or not f.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 [rot / 2] tensor")
-    rot = 2 * f.shape[0]
+    rot = 2 * f.numel()
     if rot > d:
         raise ValueError("rot = 2 * len(freqs) must not exceed the head dimension")
     return rot
 
 
 def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inverse):
-    rows = (q, k, v)
-    have = [t for t in rows if t is not None]
-    if not have:
+    first = q if q is not None else k if k is not None else v
+    if first is None:
         raise ValueError("one of q, k and v must be given")
-    first = have[0]
     if first.dim() != 4:
         raise ValueError("q, k, v must be [B, heads, T, d]")
     B, _, T, d = first.shape
@@ -107,74 +106,81 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
     in_code = _CODES.get(dtype)
     if in_code is None:
         raise TypeError("q, k, v must be float32, bfloat16 or float16, got %s" % dtype)
-    heads = [0, 0, 0]
-    strides = []
-    for i, t in enumerate(rows):
+    heads, strides, used = [], [], []
+    for t in (q, k, v):
         if t is None:
-            strides += (0, 0, 0)
+            heads.append(0)
+            strides += _NONE
             continue
         if t.dim() != 4:
             raise ValueError("q, k, v must be [B, heads, T, d]")
-        b, heads[i], n, e = t.shape
+        b, h, n, e = t.shape
         if b != B or n != T or e != d:
             raise ValueError("q, k, v must share B, T and d")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError("q, k, v must share a dtype")
         sb, sh, sn, se = t.stride()
-        if se != 1 and e > 1:
+        if se != 1 and d > 1:
             raise ValueError("the d values of a row must be contiguous")
+        heads.append(h)
         strides += (sb, sh, sn)
-    if k is not None and v is not None and heads[1] != heads[2]:
+        used.append(t)
+    if heads[1] != heads[2] and k is not None and v is not None:
         raise ValueError("k and v must have the same heads")
     rot = _check_freqs(f, d)
-    pos_stride = 0
+    pos_at, pos_stride = None, 0
     if pos is not None:
-        shape = tuple(pos.shape)
-        if pos.dtype != torch.int32 or (shape != (T,) and shape != (B, T)) or (T > 1 and pos.stride(-1) != 1):
+        shape = pos.shape
+        if pos.dtype is not torch.int32 or (shape != (B, T) and shape != (T,)) or (T > 1 and pos.stride(-1) != 1):
             raise ValueError("pos must be an int32 [T] or [B, T] tensor with its last dimension contiguous")
-        have.append(pos)
         if len(shape) == 2:
             pos_stride = pos.stride(0)
-    if out is not None:
+        pos_at = pos.data_ptr()
+        used.append(pos)
+    if f is not None:
+        used.append(f)
+    if out is None:
+        out_dtype = out_dtype or dtype
+    else:
         out = tuple(out)
         if len(out) != 3:
             raise ValueError("out must name three tensors (None for absent ones)")
-        for t, o in zip(rows, out):
+        for t, o in zip((q, k, v), out):
             if (t is None) != (o is None) or (t is not None and o.shape != t.shape):
                 raise ValueError("out must have the shapes of q, k, v")
             if o is not None:
-                if out_dtype is None:
-                    out_dtype = o.dtype
-                if o.dtype != out_dtype:
+                out_dtype = out_dtype or o.dtype
+                if o.dtype is not out_dtype:
                     raise TypeError("out must share one dtype")
-                if o.shape[3] > 1 and o.stride(3) != 1:
+                if d > 1 and o.stride(3) != 1:
                     raise ValueError("the d values of a row must be contiguous")
-                have.append(o)
-    if out_dtype is None:
-        out_dtype = dtype
+                used.append(o)
     out_code = _CODES.get(out_dtype)
     if out_code is None:
         raise TypeError("out must be float32, bfloat16 or float16, got %s" % out_dtype)
-    if f is not None:
-        have.append(f)
 
     def call(raw):
         y = out
         if y is None:
-            y = tuple([None if t is None else torch.empty(t.shape, dtype=out_dtype, device=t.device) for t in rows])
+            y = tuple([None if t is None else torch.empty_like(t, dtype=out_dtype,
+                                                               memory_format=torch.contiguous_format)
+                       for t in (q, k, v)])
+            for h in heads:
+                strides.extend((h * T * d, T * d, d))
+        else:
+            for t in y:
+                strides.extend(_NONE if t is None else t.stride()[:3])
         if B == 0 or T == 0 or not any(heads):  # nothing to turn: empty tensors have no address
             return y
-        for t in y:
-            strides.extend((0, 0, 0) if t is None else t.stride()[:3])
         st = lf_attn.load().lf_attn_rotary(
-            *[None if t is None else t.data_ptr() for t in rows + y], _I18(*strides), B, heads[0],
-            heads[1] or heads[2], T, d, None if pos is None else pos.data_ptr(), pos_stride,
-            f.data_ptr() if rot else None, rot, 1 if interleaved else 0, inverse, amplitude, in_code, out_code, raw)
+            *[None if t is None else t.data_ptr() for t in (q, k, v, *y)], _PACK18(*strides), B, heads[0],
+            heads[1] or heads[2], T, d, pos_at, pos_stride, f.data_ptr() if rot else None, rot,
+            1 if interleaved else 0, inverse, amplitude, in_code, out_code, raw)
         if st != 0:
             raise LfAttnError(st, "lf_attn_rotary")
         return y
 
-    return _on_stream(stream, have, call)
+    return _on_stream(stream, used, call)
 
 
 def fwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, *,

@@ -79,9 +79,12 @@ def test_sizes(lib):
     assert lib.lf_attn_cache_plan_bytes(1, 0, 0) > 0
     for bad in ((0, 1, 0), (1, -1, 0), (1, 1, -1), (1, 1, 1025), ((1 << 20) + 1, 1, 0)):
         assert lib.lf_attn_cache_plan_bytes(*bad) == 0
-    assert lib.lf_attn_cache_workspace_bytes(12, 12, 64, 16) > 0
-    for bad in ((12, 5, 64, 16), (0, 1, 64, 16), (12, 12, 96, 16), (256, 1, 64, 4), (12, 12, 64, 8)):
-        assert lib.lf_attn_cache_workspace_bytes(*bad) == 0
+    size = lambda ng=0, page=16, mp=1000, hq=12, hkv=12, d=64, bits=16, r=1 << 30: (  # noqa: E731
+        lib.lf_attn_cache_workspace_bytes(ng, page, mp, hq, hkv, d, bits, r))
+    assert size() > 0 and size(hq=24) > size() and size(r=5000) > 0
+    assert size(r=100) == 0 and size(mp=2) == 0        # windows, or tables, that no CTA needs help with
+    for bad in (dict(hkv=5), dict(hq=0), dict(d=96), dict(hq=256, hkv=1), dict(bits=8), dict(ng=-1)):
+        assert size(**bad) == 0
 
 
 APPEND = dict(k=FAKE, v=2 * FAKE, q=3 * FAKE, hk=None, hv=None, qo=4 * FAKE, s=i64(*[256, 64] * 6), kc=5 * FAKE, vc=6 * FAKE,
@@ -112,11 +115,11 @@ FWD_ORDER = "q o s kc vc kp vp pages page table mp plan S N ng hq hkv d r dil sc
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(ws=None), INVALID), (dict(plan=None), INVALID),
+    (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(ws=None, r=5000, mp=1000), INVALID), (dict(ws=FAKE + 8), INVALID), (dict(plan=None), INVALID),
     (dict(table=None), INVALID), (dict(scale=math.nan), INVALID), (dict(q=FAKE + 2), INVALID), (dict(o=2 * FAKE + 1), INVALID),
     (dict(o=FAKE + 128), INVALID), (dict(s=i64(260, 64, 256, 64)), INVALID), (dict(s=i64(256, 64, 0, 64)), INVALID),
     (dict(s=i64(256, -64, 256, 64)), INVALID), (dict(r=-1), INVALID), (dict(dil=i32(0, 1)), INVALID),
-    (dict(bits=4), INVALID), (dict(t=0), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(wb=1000), SMALL), (dict(N=0), OK),
+    (dict(bits=4), INVALID), (dict(t=0), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(wb=1000, r=5000, mp=1000), SMALL), (dict(N=0), OK),
 ])
 def test_attention_refusals(lib, kw, code):
     assert call(lib.lf_attn_cache_fwd, FWD, FWD_ORDER, **kw) == code
