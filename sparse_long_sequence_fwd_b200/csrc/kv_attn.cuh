@@ -19,18 +19,19 @@
 //   2c + 1, 2c + 8, 2c + 9, whose halves are paired by byte permutes.  P^T
 //   goes from accumulator to operand layout by one matrix transpose
 //   (movmatrix) per 8 keys.
-// A CTA's four warps take 16 keys each of a 64-key block; a warp keeps its own
-// running maximum, sum and O, joined through shared memory when the unit's
-// piece ends.  Each warp has a ring of kStages 16-key stages in shared memory
-// that it fills itself with cp.async, two blocks ahead of the one it computes,
+// A CTA's four warps take 16 or 32 keys each of a 64- or 128-key block; a warp
+// keeps its own running maximum, sum and O, joined through shared memory when
+// the unit's piece ends.  Each warp has a ring of stages in shared memory that
+// it fills itself with cp.async, two blocks ahead of the one it computes,
 // across unit boundaries too (short windows are a few blocks long); the page
 // table is read one block before that, and the next unit's queries while the
 // last block of a unit is computed.
 //
-// 4 bits: a group of 32 values is mid + scale (c - 8).  c - 8 is exact in bf16
-// and f16, so the MMAs run on the codes: q . k = sum over groups of
+// 4 bits: a group of 32 values is mid + scale (c - 8).  Codes are exact in bf16
+// and f16, so the MMAs run on them: q . k = sum over groups of
 // scale (q . (c - 8)) + mid (sum of q), in fp32; and for the values P scale
-// takes P's place, and the P mid are summed in fp32 beside.  With f16 queries
+// takes P's place, and the P mid are summed in fp32 beside.  Bound here:
+// instructions, half of them to spread nibbles into the MMA's operands.  With f16 queries
 // P scale may fall out of f16's range and bf16 alone would cost more than
 // f16's output rounding, so there P scale is taken in two bf16 parts (2^-17).
 //
@@ -46,21 +47,31 @@ namespace lf {
 
 constexpr int kKvWarps = 4;
 constexpr int kKvThreads = kKvWarps * 32;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
+
+// Steps of 16 keys that a warp takes at once: two over 4 bits, so that what a
+// step costs besides its keys (the walk, the vote on the base) is paid half as
+// often (instructions bound it: 102 -> 88 us at 1.6 M keys of 2 x 80 bytes);
+// one over 16 bits, where 32 rows a stage would leave an SM half the warps
+// (d = 64, batch of short windows: 7.4 against 9.1 us).
+__host__ __device__ constexpr int kv_sub(int bits) { return bits == 16 ? 1 : 2; }
+__host__ __device__ constexpr int kv_block(int bits) { return kKvWarps * 16 * kv_sub(bits); }
 
 // CTAs of four warps that an SM holds at once: by the ring's shared memory
-// (16-bit d = 64: 48 KB, d = 128: 96 KB a CTA), else by registers.
+// (16 bits: 48 KB a CTA at d = 64, 96 KB at 128), else by registers.
 __host__ __device__ constexpr int kv_ctas_per_sm(int d, int bits, bool two) {
     return d == 64 ? (two ? 3 : 4) : (bits == 16 || two ? 2 : 3);
 }
 
-// A stage: the 16 K rows, the 16 V rows, and for 4 bits their parameters.
+// A stage: for each 16 keys the K rows, the V rows, and for 4 bits their parameters.
 template <int HD, int kBits>
 struct KvStage {
+    static constexpr int kSub = kv_sub(kBits);
     static constexpr int kRow = kBits == 16 ? HD * 2 : HD / 2;
     static constexpr int kPar = kBits == 16 ? 0 : HD / 8;
     static constexpr int kV = 16 * kRow, kKp = 32 * kRow, kVp = kKp + 16 * kPar;
-    static constexpr int kBytes = kVp + 16 * kPar;
+    static constexpr int kSubBytes = kVp + 16 * kPar;
+    static constexpr int kBytes = kSub * kSubBytes;
 };
 
 struct KvAttnParams {
@@ -97,27 +108,40 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with C = 0.
+template <bool kHalf>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    if constexpr (kHalf)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
-// Four-bit codes in bits 0-3 and 16-19 of x (others ignored) -> c - 8 as two
-// 16-bit floats: the code is or'ed into the mantissa of 2^10 (f16) or 2^7
-// (bf16), and 2^10 + 8 (2^7 + 8) subtracted, both exact.
+// Four-bit codes c in bits 0-3 and 16-19 of x (others ignored) as two 16-bit
+// floats kCodeBase + c: the code or'ed into the mantissa of 2^10 (f16) or 2^7
+// (bf16).  The base is taken off again where it costs least: for K in the
+// groups' mid (mid' = mid - (base + 8) scale), for V by one more MMA with a
+// constant -(base + 8) in V's place on the same rounded P scale.  Both are
+// fp32 sums of exact products, so what that loses is 136 (1032) steps of 2^-24.
+template <bool kHalf>
+constexpr float kCodeBase = kHalf ? 1024.f : 128.f;
+constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16x2
 template <bool kHalf>
 __device__ __forceinline__ uint32_t code_pair(uint32_t x) {
-    if constexpr (kHalf) {
-        const uint32_t y = (x & 0x000f000fu) | 0x64006400u, z = 0x64086408u;
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&z));
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const uint32_t y = (x & 0x000f000fu) | 0x43004300u, z = 0x43084308u;
-        const __nv_bfloat162 h =
-            __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&z));
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
+    return (x & 0x000f000fu) | (kHalf ? 0x64006400u : 0x43004300u);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {  // zeros if not there
@@ -137,36 +161,48 @@ __device__ __forceinline__ int swz(int r) { return (((r ^ (r >> 2)) & 1) << 2) |
 // 4-bit V rows: key k's place, so that keys 2c (2c + 1, ..) are beside each other.
 __device__ __forceinline__ int v_place(int k) { return (k & 8) | ((k & 1) << 2) | ((k >> 1) & 3); }
 
-// Starts the copies of a warp's 16 keys into a stage; lane i (and i + 16)
-// has key i's row of the cache, -1: none (zeros).
+// Starts the copies of a warp's keys into a stage; lane i has key i's row of
+// the cache, -1: none (zeros).
 template <int HD, int kBits>
 __device__ __forceinline__ void kv_issue(const KvAttnParams& p, uint32_t stage, int row, int lane) {
     using St = KvStage<HD, kBits>;
-    constexpr int kChunks = St::kRow / 16;  // per row: 2, 4, 8 or 16
     if constexpr (kBits == 16) {
+        constexpr int kChunks = St::kRow / 16;  // per row: 8 or 16; 32 lanes take 32 / kChunks whole rows at a time
+        const int x = lane % kChunks;
 #pragma unroll
-        for (int i = 0; i < kChunks / 2; ++i) {  // 32 lanes take 32 / kChunks rows at a time
-            const int r = (i * 32 + lane) / kChunks, x = lane % kChunks;
-            const int at = __shfl_sync(~0u, row, r);
-            const int64_t off = at < 0 ? 0 : int64_t(at) * St::kRow + 16 * x;
+        for (int i = 0; i < kChunks / 2; ++i) {
+            const int r = (i * 32 + lane) / kChunks, at = __shfl_sync(~0u, row, r);
+            const int64_t off = int64_t(max(at, 0)) * St::kRow + 16 * x;
             const uint32_t dst = stage + r * St::kRow + 16 * (x ^ swz(r));
             cp_async16(dst, p.k + off, at >= 0);
             cp_async16(dst + St::kV, p.v + off, at >= 0);
         }
     } else {
+        // two lanes a row, 32 bytes of it at a time: an address serves a whole row
+        const int x = 16 * (lane & 1), k = lane >> 1;
 #pragma unroll
-        for (int i = 0; i < kChunks / 2; ++i) {
-            const int r = (i * 32 + lane) / kChunks, x = lane % kChunks;
-            const int at = __shfl_sync(~0u, row, r);
-            const int64_t off = at < 0 ? 0 : int64_t(at) * St::kRow + 16 * x;
-            cp_async16(stage + r * St::kRow + 16 * x, p.k + off, at >= 0);
-            cp_async16(stage + St::kV + v_place(r) * St::kRow + 16 * x, p.v + off, at >= 0);
+        for (int u = 0; u < 2; ++u) {
+            const int at = __shfl_sync(~0u, row, 16 * u + k);
+            const int64_t off = int64_t(max(at, 0)) * St::kRow + x;
+            const uint8_t *ks = p.k + off, *vs = p.v + off;
+            const uint32_t dk = stage + u * St::kSubBytes + k * St::kRow + x;
+            const uint32_t dv = stage + u * St::kSubBytes + St::kV + v_place(k) * St::kRow + x;
+#pragma unroll
+            for (int j = 0; j < St::kRow; j += 32) {
+                cp_async16(dk + j, ks + j, at >= 0);
+                cp_async16(dv + j, vs + j, at >= 0);
+            }
         }
-        const int r = lane & 15;  // lanes 0..15: K parameters, 16..31: V's
-        const uint8_t* src = (lane < 16 ? p.k_par : p.v_par) + (row < 0 ? 0 : int64_t(row) * St::kPar);
-        const uint32_t dst = stage + (lane < 16 ? St::kKp : St::kVp) + r * St::kPar;
-        if constexpr (St::kPar == 16) cp_async16(dst, src, row >= 0);
-        else cp_async8(dst, src, row >= 0);
+        // lane i: the parameters of key i
+        const int64_t off = int64_t(max(row, 0)) * St::kPar;
+        const uint32_t dst = stage + (lane >> 4) * St::kSubBytes + (lane & 15) * St::kPar;
+        if constexpr (St::kPar == 16) {
+            cp_async16(dst + St::kKp, p.k_par + off, row >= 0);
+            cp_async16(dst + St::kVp, p.v_par + off, row >= 0);
+        } else {
+            cp_async8(dst + St::kKp, p.k_par + off, row >= 0);
+            cp_async8(dst + St::kVp, p.v_par + off, row >= 0);
+        }
     }
 }
 
@@ -234,7 +270,6 @@ struct KvRegs<HD, 4> {
 __device__ __forceinline__ float2 par_of(uint32_t x) {  // (scale, mid)
     return __half22float2(*reinterpret_cast<const __half2*>(&x));
 }
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(a, fmaxf(b, c)); }
 
 // The warp's state of a unit.  Query heads 8 n + 2c and 8 n + 2c + 1 of this
 // lane are columns 0 and 1 of its n-th tile.
@@ -301,89 +336,66 @@ struct KvState {
         }
     }
 
-    // One step over the 16 keys of a stage; ok0, ok1: keys g and g + 8 are keys.
-    __device__ __forceinline__ void step(const uint8_t* stage, int g, int c, bool ok0, bool ok1, float sl2) {
+    // The scores of 16 keys: s[n][i] of key g (i < 2) or g + 8 and query head 8 n + 2c + (i & 1).
+    __device__ __forceinline__ void scores(float (&s)[kNt][4], const uint8_t* sub, int g, int c) {
         KvRegs<HD, kBits> x;
-        x.load_k(stage, g, c);
-        float s[kNt][4];
+        x.load_k(sub, g, c);
         if constexpr (kBits == 16) {
-#pragma unroll
-            for (int n = 0; n < kNt; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
 #pragma unroll
             for (int j = 0; j < HD / 32; ++j)
 #pragma unroll
                 for (int n = 0; n < kNt; ++n) {
-                    mma16816<kHalf>(s[n], x.k[0][j].x, x.k[1][j].x, x.k[0][j].y, x.k[1][j].y, q[n][2 * j][0],
-                                    q[n][2 * j][1]);
+                    if (j == 0)
+                        mma16816_first<kHalf>(s[n], x.k[0][j].x, x.k[1][j].x, x.k[0][j].y, x.k[1][j].y, q[n][0][0],
+                                              q[n][0][1]);
+                    else
+                        mma16816<kHalf>(s[n], x.k[0][j].x, x.k[1][j].x, x.k[0][j].y, x.k[1][j].y, q[n][2 * j][0],
+                                        q[n][2 * j][1]);
                     mma16816<kHalf>(s[n], x.k[0][j].z, x.k[1][j].z, x.k[0][j].w, x.k[1][j].w, q[n][2 * j + 1][0],
                                     q[n][2 * j + 1][1]);
                 }
         } else {
+            float2 sum[kNt][2];
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 uint32_t a[2][4];
+                float2 scale[2], mid[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) a[i][e] = code_pair<kHalf>(x.k[i][j] >> (4 * e));
-                const float2 p0 = par_of(x.kp[0][j]), p1 = par_of(x.kp[1][j]);
+                    const float2 f = par_of(x.kp[i][j]);
+                    const float m = fmaf(-(kCodeBase<kHalf> + 8.f), f.x, f.y);
+                    scale[i] = make_float2(f.x, f.x);
+                    mid[i] = make_float2(m, m);
+                }
 #pragma unroll
                 for (int n = 0; n < kNt; ++n) {
-                    float t[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16816<kHalf>(t, a[0][0], a[1][0], a[0][1], a[1][1], q[n][2 * j][0], q[n][2 * j][1]);
+                    float t[4];
+                    mma16816_first<kHalf>(t, a[0][0], a[1][0], a[0][1], a[1][1], q[n][2 * j][0], q[n][2 * j][1]);
                     mma16816<kHalf>(t, a[0][2], a[1][2], a[0][3], a[1][3], q[n][2 * j + 1][0], q[n][2 * j + 1][1]);
+                    const float2 w = make_float2(qs[n][j][0], qs[n][j][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 pp = i < 2 ? p0 : p1;
-                        const float u = fmaf(pp.x, t[i], pp.y * qs[n][j][i & 1]);
-                        s[n][i] = j == 0 ? u : s[n][i] + u;
+                    for (int i = 0; i < 2; ++i) {
+                        sum[n][i] = j == 0 ? fmul2(mid[i], w) : ffma2(mid[i], w, sum[n][i]);
+                        sum[n][i] = ffma2(scale[i], make_float2(t[2 * i], t[2 * i + 1]), sum[n][i]);
                     }
                 }
             }
-        }
-        // The exponent base moves only when a score exceeds it by more than
-        // 2^8 (or it has none yet): sums and O take values up to 2^8 a key.
-        bool move = false;
-#pragma unroll
-        for (int n = 0; n < kNt; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[n][i] = (i < 2 ? ok0 : ok1) ? s[n][i] * sl2 : -INFINITY;
-                move |= s[n][i] > m[n][i & 1] + 8.f;
-            }
-        if (__any_sync(~0u, move)) {
 #pragma unroll
             for (int n = 0; n < kNt; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float t = max3(m[n][e], s[n][e], s[n][2 + e]);
-                    t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
-                    t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
-                    t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
-                    const float f = t == m[n][e] ? 1.f : ex2_approx(m[n][e] - t);
-                    m[n][e] = t;
-                    l[n][e] *= f;
-#pragma unroll
-                    for (int k = 0; k < HD / 16; ++k) {
-                        o[n][k][e] *= f;
-                        o[n][k][2 + e] *= f;
-                    }
-                    if constexpr (kBits == 4)
-#pragma unroll
-                        for (int j = 0; j < kGroups; ++j) om[n][j][e] *= f;
+                for (int i = 0; i < 2; ++i) {
+                    s[n][2 * i] = sum[n][i].x;
+                    s[n][2 * i + 1] = sum[n][i].y;
                 }
         }
-#pragma unroll
-        for (int n = 0; n < kNt; ++n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[n][i] = s[n][i] == -INFINITY ? 0.f : ex2_approx(s[n][i] - m[n][i & 1]);
-                l[n][i & 1] += s[n][i];
-            }
-        }
-        x.load_v(stage, g, c);
+    }
+
+    // Adds 16 keys' values with the weights s.
+    __device__ __forceinline__ void values(const float (&s)[kNt][4], const uint8_t* sub, int g, int c) {
+        KvRegs<HD, kBits> x;
+        x.load_v(sub, g, c);
         if constexpr (kBits == 16) {
             uint32_t b[kNt][2];
 #pragma unroll
@@ -408,26 +420,23 @@ struct KvState {
         } else {
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-                const float2 p0 = par_of(x.vp[0][j]), p1 = par_of(x.vp[1][j]);
+                const float2 par[2] = {par_of(x.vp[0][j]), par_of(x.vp[1][j])};
                 uint32_t b[kNt][2], b2[kNt][2];
 #pragma unroll
-                for (int n = 0; n < kNt; ++n) {
-                    float w[4];
+                for (int n = 0; n < kNt; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 pp = i < 2 ? p0 : p1;
-                        w[i] = s[n][i] * pp.x;
-                        om[n][j][i & 1] = fmaf(s[n][i], pp.y, om[n][j][i & 1]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t hi = pack_bf16x2(w[2 * e], w[2 * e + 1]);
-                        b[n][e] = movmatrix_t(hi);
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 sp = make_float2(s[n][2 * i], s[n][2 * i + 1]);
+                        const float2 w = fmul2(sp, make_float2(par[i].x, par[i].x));
+                        const float2 m = ffma2(sp, make_float2(par[i].y, par[i].y), make_float2(om[n][j][0], om[n][j][1]));
+                        om[n][j][0] = m.x;
+                        om[n][j][1] = m.y;
+                        const uint32_t hi = pack_bf16x2(w.x, w.y);
+                        b[n][i] = movmatrix_t(hi);
                         if constexpr (kSplitP)
-                            b2[n][e] = movmatrix_t(pack_bf16x2(w[2 * e] - __uint_as_float(hi << 16),
-                                                               w[2 * e + 1] - __uint_as_float(hi & 0xffff0000u)));
+                            b2[n][i] = movmatrix_t(
+                                pack_bf16x2(w.x - __uint_as_float(hi << 16), w.y - __uint_as_float(hi & 0xffff0000u)));
                     }
-                }
                 uint32_t u[2];  // the group's unit of keys 2c, 2c + 1, and of 2c + 8, 2c + 9
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -439,11 +448,88 @@ struct KvState {
 #pragma unroll
                     for (int n = 0; n < kNt; ++n) {
                         mma16816<false>(o[n][2 * j + t], a0, a1, a2, a3, b[n][0], b[n][1]);
-                        if constexpr (kSplitP) mma16816<false>(o[n][2 * j + t], a0, a1, a2, a3, b2[n][0], b2[n][1]);
+                        mma16816<false>(o[n][2 * j + t], kMinus136, kMinus136, kMinus136, kMinus136, b[n][0], b[n][1]);
+                        if constexpr (kSplitP) {
+                            mma16816<false>(o[n][2 * j + t], a0, a1, a2, a3, b2[n][0], b2[n][1]);
+                            mma16816<false>(o[n][2 * j + t], kMinus136, kMinus136, kMinus136, kMinus136, b2[n][0], b2[n][1]);
+                        }
                     }
                 }
             }
         }
+    }
+
+    // One step over a stage; bit i of ok: there is a key i.
+    __device__ __forceinline__ void step(const uint8_t* stage, int g, int c, uint32_t ok, float sl2) {
+        constexpr int kSub = KvStage<HD, kBits>::kSub;
+        constexpr uint32_t kAll = kSub == 2 ? ~0u : 0xffffu;
+        float s[kSub][kNt][4];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            scores(s[u], stage + u * KvStage<HD, kBits>::kSubBytes, g, c);
+#pragma unroll
+            for (int n = 0; n < kNt; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[u][n][i] *= sl2;
+        }
+        if (ok != kAll) {
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (!((ok >> (16 * u + 8 * i + g)) & 1))
+#pragma unroll
+                        for (int n = 0; n < kNt; ++n) s[u][n][2 * i] = s[u][n][2 * i + 1] = -INFINITY;
+        }
+        // The exponent base moves only when a score exceeds it by more than
+        // 2^8 (or it has none yet): sums and O take values up to 2^8 a key.
+        float top[kNt][2];
+        bool move = false;
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+                if constexpr (kSub == 2) top[n][e] = fmaxf(top[n][e], fmaxf(s[kSub - 1][n][e], s[kSub - 1][n][2 + e]));
+                move |= top[n][e] > m[n][e] + 8.f;
+            }
+        if (__any_sync(~0u, move)) {
+#pragma unroll
+            for (int n = 0; n < kNt; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float t = fmaxf(m[n][e], top[n][e]);
+                    t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
+                    t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
+                    t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
+                    const float f = t == m[n][e] ? 1.f : ex2_approx(m[n][e] - t);
+                    m[n][e] = t;
+                    l[n][e] *= f;
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) {
+                        o[n][k][e] *= f;
+                        o[n][k][2 + e] *= f;
+                    }
+                    if constexpr (kBits == 4)
+#pragma unroll
+                        for (int j = 0; j < kGroups; ++j) om[n][j][e] *= f;
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float base = m[n][e] == -INFINITY ? 0.f : m[n][e];  // no score but -inf yet: weights of 0
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int i = e; i < 4; i += 2) {
+                        s[u][n][i] = ex2_approx(s[u][n][i] - base);
+                        l[n][e] += s[u][n][i];
+                    }
+            }
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) values(s[u], stage + u * KvStage<HD, kBits>::kSubBytes, g, c);
     }
 
     // The dimension of o[.][t][i] in this lane.
@@ -453,6 +539,7 @@ struct KvState {
 };
 
 // Where a CTA is in its range of the work sequence; all warps walk alike.
+template <int block>
 struct KvWalk {
     int row, unit, seq, pos, ng, head;
     int b, b1, nb;   // the next block of the unit, and where the CTA's piece of it ends
@@ -462,7 +549,7 @@ struct KvWalk {
     __device__ __forceinline__ void enter(const KvAttnParams& p) {
         head = unit / p.nsub;
         u = KvKeys(pos, ng, p.r, p.dil[head]);
-        nb = u.blocks();
+        nb = u.blocks(block);
         b1 = static_cast<int>(min(int64_t(nb), b + left));
     }
     __device__ __forceinline__ KvWalk(const KvAttnParams& p, const KvStart& s)
@@ -486,22 +573,17 @@ struct KvWalk {
         enter(p);
     }
 
-    // The row of the cache that key i = lane & 15 of the warp's part of block b is in, -1 if there is no such key.
+    // The row of the cache that key i = lane % (keys of a warp) of the warp's part of block b is in, -1: no such key.
     __device__ __forceinline__ int key_row(const KvAttnParams& p, int warp, int lane) const {
-        const int i = 16 * warp + (lane & 15);
-        int at = -1;
-        if (b < u.blocks_win) {
-            const int n = b * kKvBlock + i;
-            if (n < u.n_win) at = u.first + n * u.step;
-        } else {
-            const int n = (b - u.blocks_win) * kKvBlock + i;
-            if (n < u.ng) {
-                at = p.plan.g_list[int64_t(seq) * p.n_global + n];
-                const int back = pos - at;  // > 0
-                if (back % u.step == 0 && back / u.step < u.n_win) at = -1;  // in the window
-            }
+        constexpr int kKeys = block / kKvWarps;
+        const int n = b * block + kKeys * warp + (lane & (kKeys - 1));
+        if (n >= u.n) return -1;
+        int at = u.first + n * u.step;
+        if (n >= u.n_win) {
+            at = p.plan.g_list[int64_t(seq) * p.n_global + (n - u.n_win)];
+            const int back = pos - at;  // > 0
+            if (back % u.step == 0 && back / u.step < u.n_win) return -1;  // in the window
         }
-        if (at < 0) return -1;
         const int page = p.table[int64_t(seq) * p.max_pages + (at >> p.log_page)];
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
             atomicOr(p.status, kStatusBadCache);
@@ -532,6 +614,7 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
     kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
     constexpr int kRows = 8 * kNt;
     constexpr int kStage = KvStage<HD, kBits>::kBytes;
+    constexpr int kBlock = kv_block(kBits);
     constexpr int kUnits = 8;  // descriptors in flight: at most kStages + 2 units are between the walk and the end
     using State = KvState<HD, kBits, kHalf, kNt>;
     extern __shared__ __align__(128) uint8_t s_ring[];
@@ -550,9 +633,10 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
     uint8_t* ring = s_ring + warp * (kStages * kStage);
     const uint32_t ring_at = smem_u32(ring);
 
-    // The walk runs ahead of the blocks that are computed.  A block's meta:
-    // bits 0-15 which keys there are, bit 16 first and bit 17 last of its piece, bits 20.. the unit's descriptor.
-    KvWalk w(p, start);
+    // The walk runs ahead of the blocks that are computed.  Of each block in
+    // flight: which of the warp's keys there are, and a note: bit 0 first and
+    // bit 1 last of its piece, from bit 2 the unit's descriptor.
+    KvWalk<kBlock> w(p, start);
     int entered = 0;
     auto describe = [&](bool first_piece) {
         const bool whole = w.b == 0 && w.b1 == w.nb;
@@ -561,15 +645,15 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
             s_unit[warp][entered % kUnits] = make_int4(w.row, w.unit, 0, whole ? -1 : 2 * s + (first_piece && w.b > 0 ? 0 : 1));
     };
     int row_next = -1;
-    uint32_t meta_next = 0;
+    uint32_t note_next = 0;
     bool fresh = true;
     describe(true);
     auto fetch = [&] {
         row_next = -1;
-        meta_next = 0;
+        note_next = 0;
         if (w.left <= 0) return;
         row_next = w.key_row(p, warp, lane);
-        meta_next = (fresh ? 1u << 16 : 0u) | (w.b + 1 == w.b1 ? 1u << 17 : 0u) | uint32_t(entered % kUnits) << 20;
+        note_next = (fresh ? 1u : 0u) | (w.b + 1 == w.b1 ? 2u : 0u) | uint32_t(entered % kUnits) << 2;
         fresh = false;
         --w.left;
         if (++w.b == w.b1 && w.left > 0) {
@@ -579,21 +663,22 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
             describe(false);
         }
     };
-    uint32_t meta[kStages];
+    uint32_t ok[kStages], note[kStages];
     int64_t todo = start.n;
-    auto issue = [&](int stage, uint32_t& m) {
+    auto issue = [&](int stage, int i) {
         kv_issue<HD, kBits>(p, ring_at + stage * kStage, row_next, lane);
         cp_async_commit();
-        m = meta_next | (__ballot_sync(~0u, row_next >= 0) & 0xffffu);
+        ok[i] = __ballot_sync(~0u, row_next >= 0) & (kBlock == 64 ? 0xffffu : ~0u);
+        note[i] = note_next;
     };
     fetch();
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-        issue(i, meta[i]);
+        issue(i, i);
         fetch();
     }
     auto query = [&](uint4 (&x)[kNt][HD / 32], uint32_t m) {
-        const int4 d = s_unit[warp][m >> 20];
+        const int4 d = s_unit[warp][m >> 2];
         const int head = d.y / p.nsub, sub = d.y - head * p.nsub;
         State::load_q(x, p, static_cast<const uint8_t*>(p.q) + 2 * (d.x * p.q_row + (head * p.group + sub * p.gs) * p.q_head),
                       min(p.gs, p.group - sub * p.gs), lane);
@@ -601,21 +686,21 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
     State st;
     uint4 qn[kNt][HD / 32];
     __syncwarp();
-    query(qn, meta[0]);
+    query(qn, note[0]);
     int stage = 0;
     for (; todo > 0; --todo) {
         __syncwarp();  // every lane has read the stage that is filled next
-        issue(stage == 0 ? kStages - 1 : stage - 1, meta[kStages - 1]);
+        issue(stage == 0 ? kStages - 1 : stage - 1, kStages - 1);
         fetch();
-        const uint32_t now = meta[0];
-        if (now & (1u << 16)) st.begin(qn, lane);
+        const uint32_t now = note[0];
+        if (now & 1u) st.begin(qn, lane);
         __syncwarp();
-        if (meta[1] & (1u << 16)) query(qn, meta[1]);
+        if (note[1] & 1u) query(qn, note[1]);
         cp_async_wait<kStages - 1>();
         __syncwarp();
-        if (now & 0xffffu) st.step(ring + stage * kStage, g, c, (now >> g) & 1, (now >> (g + 8)) & 1, p.sl2);
-        if (now & (1u << 17)) {  // join the lanes' and the warps' states
-            const int4 d = s_unit[warp][now >> 20];
+        if (ok[0]) st.step(ring + stage * kStage, g, c, ok[0], p.sl2);
+        if (now & 2u) {  // join the lanes' and the warps' states
+            const int4 d = s_unit[warp][now >> 2];
             const int head = d.y / p.nsub, sub = d.y - head * p.nsub;
             const int heads = min(p.gs, p.group - sub * p.gs), qh = head * p.group + sub * p.gs;
 const int join = min(p.gs, 8) * kJoinRow;  // floats of a warp
@@ -688,7 +773,10 @@ const int join = min(p.gs, 8) * kJoinRow;  // floats of a warp
             }
         }
 #pragma unroll
-        for (int i = 0; i + 1 < kStages; ++i) meta[i] = meta[i + 1];
+        for (int i = 0; i + 1 < kStages; ++i) {
+            ok[i] = ok[i + 1];
+            note[i] = note[i + 1];
+        }
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();

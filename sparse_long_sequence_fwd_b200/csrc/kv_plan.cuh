@@ -10,11 +10,11 @@
 // blocks [s W / G', (s + 1) W / G') of all W, so every CTA has the same number
 // of blocks, give or take one, however ragged the lengths are.  A unit that a
 // range boundary cuts leaves a partial state in every CTA that has a piece of
-// it, and a merge kernel joins them.  G' = min(G, ceil(W / 4)): a CTA's start
-// and a piece's end cost as much as a few blocks.
+// it, and a merge kernel joins them.  G' gives a CTA at least kKvMinKeys
+// keys: its start and a piece's end cost as much as a few blocks.
 //
-// When no ordinary unit has more than kKvWholeBlocks blocks (a window, known
-// on the host), units stay whole: a CTA takes the units that begin in its
+// When no ordinary unit has more than kKvWholeKeys keys (a window, known on
+// the host), units stay whole: a CTA takes the units that begin in its
 // range, and nothing is merged.  (A global row, which sees every key, is then
 // one CTA's work too.)
 //
@@ -27,11 +27,10 @@
 
 namespace lf {
 
-constexpr int kKvBlock = 64;           // keys per block of the work sequence
 constexpr int kKvMaxGlobal = 1024;     // global tokens per sequence (the lists are ranked in O(n^2))
 constexpr int kKvMaxCtas = 2048;
-constexpr int kKvMinBlocks = 4;        // blocks per CTA below which fewer CTAs take part
-constexpr int kKvWholeBlocks = 16;
+constexpr int kKvMinKeys = 256;        // keys per CTA below which fewer CTAs take part
+constexpr int kKvWholeKeys = 1024;
 constexpr int kPlanThreads = 1024;
 constexpr uint32_t kStatusBadCache = 4u;  // a row or page of a cache call outside its range (left out)
 constexpr uint32_t kStatusBadPlan = 8u;   // a cache call with another plan than its arguments say
@@ -61,6 +60,7 @@ struct KvPlan {  // views into the caller's plan buffer
 struct KvShape {  // what a plan is made for
     int S, N, n_global, max_len;
     int q_heads, kv_heads, nsub, r, G;
+    int block;           // keys per block
     int cut;             // 0: units stay whole
     uint64_t sig_rows, sig_all;
     int32_t dil[kMaxHeads];
@@ -99,20 +99,19 @@ inline KvPlan kv_plan_view(void* buf, const KvPlanLayout& L) {
     return p;
 }
 
-// A unit's keys.  Window key n of n_win sits at position first + n * step; the
-// blocks of the global list follow (entries inside the window are left out
-// there, so each key counts once).
+// A unit's keys: window key n < n_win sits at position first + n * step, key
+// n_win + a is entry a of the global list (an entry inside the window is left
+// out there, so each key counts once).
 struct KvKeys {
-    int first, step, n_win, blocks_win, ng;
+    int first, step, n_win, n;
     __host__ __device__ KvKeys(int pos, int ng_row, int r, int dil) {
         step = ng_row < 0 ? 1 : dil;
         const int back = ng_row < 0 ? pos : (pos / dil < r ? pos / dil : r);
         n_win = back + 1;
         first = pos - back * step;
-        blocks_win = (n_win + kKvBlock - 1) / kKvBlock;
-        ng = ng_row < 0 ? 0 : ng_row;
+        n = n_win + (ng_row < 0 ? 0 : ng_row);
     }
-    __host__ __device__ int blocks() const { return blocks_win + (ng + kKvBlock - 1) / kKvBlock; }
+    __host__ __device__ int blocks(int block) const { return (n + block - 1) / block; }
 };
 
 // Sorts a sequence's global tokens, each once.  grid: S; smem: 2 n_global ints.
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
                     }
                     ng = (a < cnt && g[a] == pos) ? -1 : a;
                 }
-                for (int h = 0; h < sh.kv_heads; ++h) blocks += KvKeys(pos, ng, sh.r, sh.dil[h]).blocks();
+                for (int h = 0; h < sh.kv_heads; ++h) blocks += KvKeys(pos, ng, sh.r, sh.dil[h]).blocks(sh.block);
                 blocks *= sh.nsub;
             }
             p.row_seq[n] = seq;
@@ -236,7 +235,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
     }
     __syncthreads();
     // The split.  Block x of the sequence: its row, unit, and place in the unit.
-    const int64_t wide = (W + kKvMinBlocks - 1) / kKvMinBlocks;
+    const int64_t wide = (W * sh.block + kKvMinKeys - 1) / kKvMinKeys;
     const int64_t G = wide < sh.G ? wide : sh.G;  // no CTA below G has an empty range
     auto locate = [&](int64_t x, KvStart& at, int64_t& unit_first, int64_t& unit_end) {
         int lo = 0, hi = sh.N;  // the last row with prefix <= x (rows without blocks are passed over)
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
         at.ng = p.row_ng[lo];
         int unit = 0, nb = 1;
         for (int h = 0; h < sh.kv_heads; ++h) {
-            nb = KvKeys(at.pos, at.ng, sh.r, sh.dil[h]).blocks();
+            nb = KvKeys(at.pos, at.ng, sh.r, sh.dil[h]).blocks(sh.block);
             const int64_t all = int64_t(nb) * sh.nsub;
             if (left < all) {
                 unit = h * sh.nsub + static_cast<int>(left / nb);

@@ -71,11 +71,11 @@ bool by_eight(const void* p, int dims, const int64_t* s, size_t es) {
     return true;
 }
 
-// Tokens per CTA: about kRotItems items, but no fewer CTAs than two per SM.
-int tile_for(int64_t tokens, int items_per_token) {
-    const int64_t spread = (tokens + 295) / 296;
+// Tokens per CTA: as many as a CTA's threads hold at once, but no fewer CTAs than two per SM.
+int tile_for(int64_t tokens, int items_per_token, size_t element) {
+    const int64_t held = int64_t(kRotThreads) * (8 / int(element)), spread = (tokens + 295) / 296;
     return static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>({int64_t(kRotMaxTile), int64_t(kRotItems) / std::max(1, items_per_token), spread})));
+        1, std::min<int64_t>({int64_t(kRotMaxTile), held / std::max(1, items_per_token), spread})));
 }
 
 template <typename Tin, typename Tout>
@@ -117,9 +117,10 @@ lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_he
     for (int h = 0; h < kv_heads; ++h) sh->dil[h] = dil ? std::min(dil[h], sh->max_len) : 1;
     // no more CTAs than blocks that ordinary rows can have
     const int64_t keys = std::min<int64_t>(int64_t(sh->r) + 1, sh->max_len);
-    const int64_t blocks = (keys + kKvBlock - 1) / kKvBlock + (n_global + kKvBlock - 1) / kKvBlock;
+    sh->block = kv_block(bits);
+    const int64_t blocks = (keys + n_global + sh->block - 1) / sh->block;
     const int64_t grid = kv_grid(d, bits, heads_of_unit(group, sh->nsub));
-    sh->cut = blocks > kKvWholeBlocks;
+    sh->cut = blocks * sh->block > kKvWholeKeys;
     sh->G = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(grid, blocks * std::min<int64_t>(N, grid) * kv_heads * sh->nsub)));
     uint64_t h = 14695981039346656037ull;
@@ -237,9 +238,11 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
     p.inter = interleaved ? 1 : 0;
     p.back = inverse ? 1 : 0;
     p.amp = amplitude;
-    p.tile = tile_for(int64_t(B) * T, heads * (vec ? d / 16 : d));
-    const dim3 grid((T + p.tile - 1) / p.tile, B);
-    const size_t smem = size_t(p.tile) * (rot / 2) * sizeof(float2);
+    p.per = small_div(vec ? d / 16 : d);
+    const int tile = tile_for(int64_t(B) * T, heads * p.per.by, ei);
+    p.tile = small_div(tile);
+    const dim3 grid((T + tile - 1) / tile, B);
+    const size_t smem = size_t(tile) * (rot / 2) * sizeof(float2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (in_dtype == LF_F32 && out_dtype == LF_F32) launch_rotary<float, float>(p, vec, grid, smem, s);
     else if (in_dtype == LF_F32 && out_dtype == LF_BF16) launch_rotary<float, __nv_bfloat16>(p, vec, grid, smem, s);
@@ -337,11 +340,13 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     p.inter = interleaved ? 1 : 0;
     p.amp = amplitude;
     p.sig = sh.sig_rows;
-    p.tile = tile_for(n_tokens, (2 * kv_heads + p.heads[2]) * (vec ? d / 16 : d));
+    p.per = small_div(vec ? d / 16 : d);
+    int tile = tile_for(n_tokens, (2 * kv_heads + p.heads[2]) * p.per.by, 2);
     const size_t staged = bits == 4 ? size_t(2) * kv_heads * d * 2 : 0;  // per token
-    while (p.tile > 1 && staged * p.tile > size_t(kAppendTileSmem)) --p.tile;
-    const size_t smem = ((size_t(p.tile) * (rot / 2) * sizeof(float2) + 15) & ~size_t(15)) + staged * p.tile;
-    const unsigned grid = (n_tokens + p.tile - 1) / p.tile;
+    while (tile > 1 && staged * tile > size_t(kAppendTileSmem)) --tile;
+    p.tile = small_div(tile);
+    const size_t smem = ((size_t(tile) * (rot / 2) * sizeof(float2) + 15) & ~size_t(15)) + staged * tile;
+    const unsigned grid = (n_tokens + tile - 1) / tile;
     void (*kern)(KvAppendParams);
     if (dtype == LF_F16)
         kern = bits == 16 ? (vec ? kv_append_kernel<__half, 16, true> : kv_append_kernel<__half, 16, false>)

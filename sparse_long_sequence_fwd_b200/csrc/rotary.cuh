@@ -17,8 +17,10 @@
 // the kernels are copies that must not be slowed down by the trigonometry.
 // A CTA takes a few tokens over all heads: the sines of a token are computed
 // once into shared memory and serve its q and k heads (36 rows a token at
-// 12 heads), and a thread moves 16 values at a time (two 8-value chunks that
-// are turned against each other), several of them in flight.
+// 12 heads).  A thread moves items of 16 values (two 8-value chunks that are
+// turned against each other); the loads of a CTA's first 1024 items (512 from
+// fp32), which is all of them where a token has no more, are in flight before
+// the sines are computed, so the two overlap.
 #pragma once
 #include "lf_common.cuh"
 #include "ptx.cuh"
@@ -27,18 +29,35 @@ namespace lf {
 
 constexpr int kRotThreads = 256;
 constexpr int kRotMaxD = 256;
-constexpr int kRotItems = 1024;   // 16-value items per CTA that the tile of tokens aims at
 constexpr int kRotMaxTile = 16;   // tokens per CTA
 
+// 16-value items that a thread holds at once: 128 bytes of either type.
+template <typename T>
+constexpr int kRotItems = 8 / int(sizeof(T));
+
+// x / by for x < 2^20 and by <= 256: magic = ceil(2^32 / by), unused for 1.
+struct SmallDiv {
+    uint32_t by, magic;
+    __device__ __forceinline__ int div(int x) const { return by == 1 ? x : int(__umulhi(uint32_t(x), magic)); }
+};
+inline SmallDiv small_div(int by) {
+    return SmallDiv{uint32_t(by), by == 1 ? 0u : uint32_t((0x100000000ull + by - 1) / by)};
+}
+
+// Eight values as loaded (kU 16-byte words), widened, and stored.
 template <typename T>
 struct RowIo;
 template <>
 struct RowIo<float> {
-    static __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-        const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    static constexpr int kU = 2;
+    static __device__ __forceinline__ void widen(const uint4* a, float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[4 * i] = __uint_as_float(a[i].x);
+            v[4 * i + 1] = __uint_as_float(a[i].y);
+            v[4 * i + 2] = __uint_as_float(a[i].z);
+            v[4 * i + 3] = __uint_as_float(a[i].w);
+        }
     }
     static __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
         reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -49,14 +68,9 @@ struct RowIo<float> {
 };
 template <>
 struct RowIo<__nv_bfloat16> {
-    static __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-        widen(__ldcs(reinterpret_cast<const uint4*>(p)), v);
-    }
-    static __device__ __forceinline__ void load8_shared(const __nv_bfloat16* p, float (&v)[8]) {
-        widen(*reinterpret_cast<const uint4*>(p), v);
-    }
-    static __device__ __forceinline__ void widen(uint4 a, float (&v)[8]) {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    static constexpr int kU = 1;
+    static __device__ __forceinline__ void widen(const uint4* a, float (&v)[8]) {
+        const uint32_t w[4] = {a->x, a->y, a->z, a->w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // bf16 is the upper half of fp32
             v[2 * i] = __uint_as_float(w[i] << 16);
@@ -72,14 +86,9 @@ struct RowIo<__nv_bfloat16> {
 };
 template <>
 struct RowIo<__half> {
-    static __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-        widen(__ldcs(reinterpret_cast<const uint4*>(p)), v);
-    }
-    static __device__ __forceinline__ void load8_shared(const __half* p, float (&v)[8]) {
-        widen(*reinterpret_cast<const uint4*>(p), v);
-    }
-    static __device__ __forceinline__ void widen(uint4 a, float (&v)[8]) {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    static constexpr int kU = 1;
+    static __device__ __forceinline__ void widen(const uint4* a, float (&v)[8]) {
+        const uint32_t w[4] = {a->x, a->y, a->z, a->w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -153,6 +162,41 @@ __device__ __forceinline__ float turn_one(At at, int e, int rot, bool inter, con
     return first ? x * cs[i].x - y * cs[i].y : x * cs[i].x + y * cs[i].y;
 }
 
+// A CTA's items 0 .. n-1, a thread's share of kRotItems at a time: source(i,
+// e0, e1) gives the row and the two chunks' places in it (null: no such
+// item), sink(i, e0, e1, u, v) takes the widened chunks.  ready() runs once,
+// when the first loads are under way.
+template <typename T, typename Source, typename Ready, typename Sink>
+__device__ __forceinline__ void move_items(int n, Source source, Ready ready, Sink sink) {
+    constexpr int kItems = kRotItems<T>, kU = RowIo<T>::kU;
+    for (int i0 = 0; i0 < n; i0 += kItems * kRotThreads) {
+        uint4 raw[kItems][2][kU];
+        int e0[kItems], e1[kItems];
+        bool there[kItems];
+#pragma unroll
+        for (int a = 0; a < kItems; ++a) {
+            const int i = i0 + a * kRotThreads + threadIdx.x;
+            const T* x = i < n ? source(i, e0[a], e1[a]) : nullptr;
+            there[a] = x != nullptr;
+            if (there[a])
+#pragma unroll
+                for (int w = 0; w < kU; ++w) {
+                    raw[a][0][w] = __ldcs(reinterpret_cast<const uint4*>(x + e0[a]) + w);
+                    raw[a][1][w] = __ldcs(reinterpret_cast<const uint4*>(x + e1[a]) + w);
+                }
+        }
+        if (i0 == 0) ready();
+#pragma unroll
+        for (int a = 0; a < kItems; ++a)
+            if (there[a]) {
+                float u[8], v[8];
+                RowIo<T>::widen(raw[a][0], u);
+                RowIo<T>::widen(raw[a][1], v);
+                sink(i0 + a * kRotThreads + threadIdx.x, e0[a], e1[a], u, v);
+            }
+    }
+}
+
 // ------------------------------------------------------------ dense rows
 
 struct RotaryParams {
@@ -164,7 +208,8 @@ struct RotaryParams {
     const int32_t* pos;  // [B][T] (stride pos_stride, 0: shared), or null: 0 .. T-1
     int64_t pos_stride;
     const double* freqs;
-    int B, T, d, rot, tile;
+    int B, T, d, rot;
+    SmallDiv tile, per;  // tokens per CTA; items (kVec) or values per row
     int inter, back;
     float amp;
 };
@@ -173,23 +218,23 @@ struct RotaryParams {
 template <typename Tin, typename Tout, bool kVec>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
     extern __shared__ float2 s_cs[];  // [tile][rot/2]
-    const int b = blockIdx.y, t0 = blockIdx.x * p.tile;
-    const int nt = min(p.tile, p.T - t0), half = p.rot / 2;
-    for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
-        const int t = i / half, f = i - t * half;
-        const int pos = p.pos ? p.pos[b * p.pos_stride + t0 + t] : t0 + t;
-        s_cs[i] = turn_of(pos, p.freqs[f], p.amp, p.back);
-    }
-    __syncthreads();
-    const int heads = p.heads[0] + p.heads[1] + p.heads[2];
-    const int per = kVec ? p.d / 16 : p.d;  // items per row
-    const int n = heads * nt * per;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kRotThreads) {
-        const int row = i / per, it = i - row * per;
-        int h = row / nt;
-        const int t = row - h * nt;
-        int w = 0;
+    const int b = blockIdx.y, tile = p.tile.by, per = p.per.by, t0 = blockIdx.x * tile;
+    const int nt = min(tile, p.T - t0), half = p.rot / 2;
+    auto ready = [&] {
+        for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
+            const int t = i / half, f = i - t * half;
+            const int pos = p.pos ? p.pos[b * p.pos_stride + t0 + t] : t0 + t;
+            s_cs[i] = turn_of(pos, p.freqs[f], p.amp, p.back);
+        }
+        __syncthreads();
+    };
+    // item or value i: a row (head of q, k or v, and token) and the place in it
+    auto place = [&](int i, int& w, int& h, int& t, int& it) {
+        const int row = p.per.div(i);
+        it = i - row * per;
+        h = p.tile.div(row);
+        t = row - h * tile;
+        w = 0;
         if (h >= p.heads[0]) {
             h -= p.heads[0];
             w = 1;
@@ -198,21 +243,41 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
                 w = 2;
             }
         }
-        const Tin* x = static_cast<const Tin*>(p.x[w]) + b * p.xs[w][0] + h * p.xs[w][1] + (t0 + t) * p.xs[w][2];
-        Tout* y = static_cast<Tout*>(p.y[w]) + b * p.ys[w][0] + h * p.ys[w][1] + (t0 + t) * p.ys[w][2];
-        const int rot = w == 2 ? 0 : p.rot;  // v is copied
-        if constexpr (kVec) {
-            int e0, e1;
-            item_at(it, rot, p.inter, e0, e1);
-            float u[8], v[8];
-            RowIo<Tin>::load8(x + e0, u);
-            RowIo<Tin>::load8(x + e1, v);
-            turn_item(u, v, e0, e1, rot, p.inter, s_cs + t * half);
-            RowIo<Tout>::store8(y + e0, u);
-            RowIo<Tout>::store8(y + e1, v);
-        } else {
-            RowIo<Tout>::store(y + it, turn_one([&](int e) { return RowIo<Tin>::load(x + e); }, it, rot, p.inter,
-                                                s_cs + t * half));
+    };
+    auto from = [&](int w, int h, int t) {
+        return static_cast<const Tin*>(p.x[w]) + b * p.xs[w][0] + h * p.xs[w][1] + (t0 + t) * p.xs[w][2];
+    };
+    auto to = [&](int w, int h, int t) {
+        return static_cast<Tout*>(p.y[w]) + b * p.ys[w][0] + h * p.ys[w][1] + (t0 + t) * p.ys[w][2];
+    };
+    const int n = (p.heads[0] + p.heads[1] + p.heads[2]) * tile * per;
+    if constexpr (kVec) {
+        move_items<Tin>(
+            n,
+            [&](int i, int& e0, int& e1) -> const Tin* {
+                int w, h, t, it;
+                place(i, w, h, t, it);
+                item_at(it, w == 2 ? 0 : p.rot, p.inter, e0, e1);
+                return t < nt ? from(w, h, t) : nullptr;
+            },
+            ready,
+            [&](int i, int e0, int e1, float(&u)[8], float(&v)[8]) {
+                int w, h, t, it;
+                place(i, w, h, t, it);
+                turn_item(u, v, e0, e1, w == 2 ? 0 : p.rot, p.inter, s_cs + t * half);  // v is copied
+                Tout* y = to(w, h, t);
+                RowIo<Tout>::store8(y + e0, u);
+                RowIo<Tout>::store8(y + e1, v);
+            });
+    } else {
+        ready();
+        for (int i = threadIdx.x; i < n; i += kRotThreads) {
+            int w, h, t, it;
+            place(i, w, h, t, it);
+            if (t >= nt) continue;
+            const Tin* x = from(w, h, t);
+            RowIo<Tout>::store(to(w, h, t) + it, turn_one([&](int e) { return RowIo<Tin>::load(x + e); }, it,
+                                                          w == 2 ? 0 : p.rot, p.inter, s_cs + t * half));
         }
     }
 }

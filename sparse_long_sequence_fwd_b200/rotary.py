@@ -70,7 +70,7 @@ def _on_stream(stream: Optional[torch.cuda.Stream], tensors, call):
         if t.get_device() != index:
             raise ValueError("all tensors must be on one device")
     if stream is None:
-        if torch.cuda.current_device() == index:
+        if torch._C._cuda_getDevice() == index:
             return call(torch._C._cuda_getCurrentRawStream(index))
         with torch.cuda.device(index):
             return call(torch._C._cuda_getCurrentRawStream(index))
@@ -106,24 +106,23 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
     in_code = _CODES.get(dtype)
     if in_code is None:
         raise TypeError("q, k, v must be float32, bfloat16 or float16, got %s" % dtype)
-    heads, strides, used = [], [], []
-    for t in (q, k, v):
+    rows, heads, strides, used = (q, k, v), [], [], []
+    for t in rows:
         if t is None:
             heads.append(0)
             strides += _NONE
             continue
-        if t.dim() != 4:
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 4:
             raise ValueError("q, k, v must be [B, heads, T, d]")
-        b, h, n, e = t.shape
-        if b != B or n != T or e != d:
+        if shape[0] != B or shape[2] != T or shape[3] != d:
             raise ValueError("q, k, v must share B, T and d")
         if t.dtype is not dtype:
             raise TypeError("q, k, v must share a dtype")
-        sb, sh, sn, se = t.stride()
-        if se != 1 and d > 1:
+        if stride[3] != 1 and d > 1:
             raise ValueError("the d values of a row must be contiguous")
-        heads.append(h)
-        strides += (sb, sh, sn)
+        heads.append(shape[1])
+        strides += stride[:3]
         used.append(t)
     if heads[1] != heads[2] and k is not None and v is not None:
         raise ValueError("k and v must have the same heads")
@@ -145,7 +144,7 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
         out = tuple(out)
         if len(out) != 3:
             raise ValueError("out must name three tensors (None for absent ones)")
-        for t, o in zip((q, k, v), out):
+        for t, o in zip(rows, out):
             if (t is None) != (o is None) or (t is not None and o.shape != t.shape):
                 raise ValueError("out must have the shapes of q, k, v")
             if o is not None:
@@ -162,18 +161,18 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
     def call(raw):
         y = out
         if y is None:
-            y = tuple([None if t is None else torch.empty_like(t, dtype=out_dtype,
-                                                               memory_format=torch.contiguous_format)
-                       for t in (q, k, v)])
-            for h in heads:
-                strides.extend((h * T * d, T * d, d))
+            kw = {} if out_dtype is dtype else {"dtype": out_dtype}
+            y = tuple([None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format, **kw)
+                       for t in rows])
+            n = T * d
+            strides.extend((heads[0] * n, n, d, heads[1] * n, n, d, heads[2] * n, n, d))
         else:
             for t in y:
                 strides.extend(_NONE if t is None else t.stride()[:3])
         if B == 0 or T == 0 or not any(heads):  # nothing to turn: empty tensors have no address
             return y
         st = lf_attn.load().lf_attn_rotary(
-            *[None if t is None else t.data_ptr() for t in (q, k, v, *y)], _PACK18(*strides), B, heads[0],
+            *[None if t is None else t.data_ptr() for t in rows + y], _PACK18(*strides), B, heads[0],
             heads[1] or heads[2], T, d, pos_at, pos_stride, f.data_ptr() if rot else None, rot,
             1 if interleaved else 0, inverse, amplitude, in_code, out_code, raw)
         if st != 0:
