@@ -209,7 +209,8 @@ lf_status lf_attn_merge_rows(const float* ml, const float* acc, int n_parts, int
  *   strides     HOST int64 [18]: (sample, head, token) strides in elements of
  *               q, k, v, q_out, k_out, v_out; the d values of a row are
  *               contiguous.  Strides of inputs may be 0, those of outputs
- *               not; no output may overlap an input.
+ *               not; no output may overlap an input.  Head and token strides
+ *               are below 2^31.
  *   B, T, q_heads, kv_heads   sizes; B and T may be 0
  *   d           1..256;  rot: even, 0..d (0: a copy; freqs may be NULL)
  *   pos         DEVICE int32, [T] per sample at a stride of pos_stride (0:
@@ -280,13 +281,13 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  *   k_held, v_held   DEVICE dense rows for what the cache now holds (the
  *               dequantised values for bits 4), or NULL
  *   strides     HOST int64 [12]: (token, head) strides in elements of k, v,
- *               q, k_held, v_held, q_out (those of NULL rows are not read);
- *               no output may overlap an input
+ *               q, k_held, v_held, q_out (those of NULL rows are not read),
+ *               below 2^31; no output may overlap an input
  *   rot == 0    leaves keys and queries as they are
  *   4 bits: scale = fp16((max - min) / 15), mid = fp16(min + 8 scale), c =
  *   (x - mid) / scale + 8 rounded to the nearest, ties to even (8 where scale
- *   is 0), x being the turned value in `dtype`.  Scale and mid have fp16's
- *   range; a group with an infinity or a NaN is held as NaN.
+ *   is 0), x being the turned value in `dtype`.  A group with an infinity or a
+ *   NaN, or whose scale or mid is past fp16's range, is held as NaN.
  *
  * lf_attn_cache_fwd -- the attention of the step's rows over the cache, which
  * already holds their own keys.  q and out: DEVICE rows

@@ -7,8 +7,9 @@
 //   scale = fp16((max - min) / 15), mid = fp16(min + 8 scale),
 //   c = clamp(round((x - mid) / scale) + 8, 0, 15)   (ties to even; 8 if scale is 0)
 // and the group stands for mid + scale (c - 8).  A group with an infinity or
-// a NaN is held as NaN (mid).  Near a border between codes the subtraction
-// and the division are IEEE ones, so that the codes are the formula's.
+// a NaN, or whose scale or mid is past fp16's range, is held as NaN (mid).
+// Near a border between codes the subtraction and the division are IEEE ones,
+// so that the codes are the formula's.
 //
 // Bound: bytes, as rotary.cuh.  For 4 bits a CTA's turned rows pass through
 // shared memory (16-bit), where four neighbouring lanes take the 32 values
@@ -25,9 +26,9 @@ namespace lf {
 
 struct KvAppendParams {
     const void* x[3];  // k, v, q rows [N][heads][d]; q may be absent
-    int64_t xs[3][2];  // (token, head), elements
     void* y[3];        // dense copies: held k, held v (may be absent), turned q
-    int64_t ys[3][2];
+    int xt[3], xh[3];  // token and head strides, elements
+    int yt[3], yh[3];
     int heads[3];
     uint8_t* cache[2];  // k, v
     uint8_t* par[2];    // 4 bits
@@ -36,63 +37,74 @@ struct KvAppendParams {
     uint32_t* status;
     const double* freqs;  // null: no turn (rot == 0)
     int N, d, rot, n_pages, log_page, max_pages, inter;
-    SmallDiv tile, per;
+    int log_tile, per;
     float amp;
     uint64_t sig;
 };
 
-// A tile's tokens.
+// A tile's tokens: whether they are one, and the row of the cache of their kv
+// head 0 (head h's is h pages' rows further), -1: none.
 struct KvSlots {
-    int seq[kRotMaxTile], slot[kRotMaxTile];  // slot: page << log_page | place, -1: none
+    int live[kRotMaxTile], row[kRotMaxTile];
 };
 
-__device__ __forceinline__ int64_t kv_cache_row(int slot, int log_page, int kv_heads, int h) {
-    const int page = slot >> log_page;
-    return (int64_t(int64_t(page) * kv_heads + h) << log_page) + (slot & ((1 << log_page) - 1));
+// Minimum and maximum of 8 values of a 16-bit type, pairwise; NaN if there is one.
+template <typename T>
+__device__ __forceinline__ void range8(uint4 x, float& lo, float& hi) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const T2* v = reinterpret_cast<const T2*>(&x);
+    T2 a = __hmin2_nan(__hmin2_nan(v[0], v[1]), __hmin2_nan(v[2], v[3]));
+    T2 b = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+        a = __hmin2_nan(a, __shfl_xor_sync(~0u, a, o));
+        b = __hmax2_nan(b, __shfl_xor_sync(~0u, b, o));
+    }
+    a = __hmin2_nan(a, __lowhigh2highlow(a));
+    b = __hmax2_nan(b, __lowhigh2highlow(b));
+    lo = float(a.x);
+    hi = float(b.x);
 }
 
 // Four lanes (lane & 3 = cc) hold the 32 values of group gr of a row, eight
-// each.  All lanes of the warp take part; `on`: this lane has values.
-// A code is x' = (x - mid) / scale rounded: the quotient by the reciprocal is
-// off by under 2^-19 (values of at most 8.1, three roundings), so only one
-// that close to a border between codes is divided for.
-__device__ __forceinline__ void quantise8(const float (&x)[8], bool is_k, bool on, int cc, int gr, int groups,
-                                          uint8_t* codes, uint8_t* par, float& scale, float& mid, uint32_t& w) {
-    float lo = x[0], hi = x[0], bad = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        bad = fmaf(x[i], 0.f, bad);  // 0, or NaN for infinities and NaN
-    }
-#pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
-        bad += __shfl_xor_sync(~0u, bad, o);
-    }
+// each (raw); all lanes of the warp take part, `on` ones have somewhere to
+// put codes and parameters.  Gives the eight codes - 8, scale and mid.
+// (x - mid) / scale clamped to a code and rounded: u = (x - mid) / (15 scale) +
+// 8 / 15 saturates to 0..1 and 15 u is rounded by adding 1.5 * 2^23.  15 u is
+// off by under 2^-18 (the reciprocal, its fifteenth, the sum, its constant),
+// and only where it is that close to a border the group divides.
+template <typename T>
+__device__ __forceinline__ void quantise8(uint4 raw, bool is_k, bool on, int cc, int gr, int groups, uint8_t* codes,
+                                          uint8_t* par, float& scale, float& mid, float (&c8)[8]) {
+    float lo, hi, x[8];
+    range8<T>(raw, lo, hi);
+    RowIo<T>::widen(&raw, x);
     const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
     scale = __half2float(hs);
     __half hm = __float2half_rn(__fadd_rn(lo, __fmul_rn(8.f, scale)));
-    if (bad != bad) hm = __float2half_rn(bad);
+    if (!(scale < INFINITY) || !(fabsf(__half2float(hm)) < INFINITY)) hm = __float2half_rn(NAN);
     mid = __half2float(hm);
-    const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;  // scale 0: all codes 8
-    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
-    w = 0;
-    bool near = false;
+    const float inv = scale > 0.f ? __fdividef(1.f, 15.f * scale) : 0.f;  // scale 0: all codes 8
+    constexpr float kRound = 12582912.f;
+    uint32_t w = 0;
+    float off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], mid), inv), -8.f), 7.f);
-        const float r = __fadd_rn(q, kRound + 8.f);
-        near |= fabsf(__fsub_rn(q, __fsub_rn(r, kRound + 8.f))) > 0.5f - 1.f / 262144.f;
-        w |= (__float_as_uint(r) & 15u) << (4 * i);
+        const float u = __saturatef(fmaf(__fsub_rn(x[i], mid), inv, 8.f / 15.f));
+        const float r = fmaf(u, 15.f, kRound);
+        const float whole = r - kRound;
+        off = fmaxf(off, fabsf(fmaf(u, 15.f, -whole)));
+        c8[i] = whole - 8.f;
+        w += (__float_as_uint(r) - __float_as_uint(kRound)) << (4 * i);
     }
-    if (near && scale > 0.f) {
+    if (off > 0.5f - 1.f / 131072.f && scale > 0.f) {
         w = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float q = fminf(fmaxf(__fdiv_rn(__fsub_rn(x[i], mid), scale), -8.f), 7.f);
-            w |= (__float_as_uint(__fadd_rn(q, kRound + 8.f)) & 15u) << (4 * i);
+            const float q = rintf(__fdiv_rn(__fsub_rn(x[i], mid), scale)) + 8.f;
+            const float c = fminf(fmaxf(q, 0.f), 15.f);
+            c8[i] = c - 8.f;
+            w |= static_cast<uint32_t>(c) << (4 * i);
         }
     }
     // V: units [r][g], r = 2 cc (low half of w) and 2 cc + 1; the lane of the neighbouring
@@ -110,132 +122,133 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], bool is_k, bool o
             uint32_t(__half_as_ushort(hs)) | uint32_t(__half_as_ushort(hm)) << 16;
 }
 
-// grid: tiles of tokens.  smem: (cos, sin) [tile][rot/2]; 4 bits: the turned
-// k and v rows [k heads + v heads][tile][d] in 16 bits.
+// grid: tiles of tokens.  smem: (cos, sin) [tile][cs_stride]; 4 bits: the
+// turned k and v rows [k heads + v heads][tile][d] in 16 bits.
 template <typename T, int kBits, bool kVec>
-__global__ void __launch_bounds__(kRotThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
     extern __shared__ __align__(16) uint8_t s_raw[];
     __shared__ KvSlots sl;
     if (p.plan.sig[0] != p.sig) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadPlan);
         return;
     }
-    const int tile = p.tile.by, per = p.per.by;
-    const int n0 = blockIdx.x * tile, nt = min(tile, p.N - n0), half = p.rot / 2;
+    const int tile = 1 << p.log_tile, n0 = blockIdx.x * tile;
+    const int nt = min(tile, p.N - n0), half = p.rot / 2, stride = cs_stride(half), kv = p.heads[0];
     float2* s_cs = reinterpret_cast<float2*>(s_raw);
-    T* s_row = reinterpret_cast<T*>(s_raw + ((size_t(tile) * half * 8 + 15) & ~size_t(15)));
+    T* s_row = reinterpret_cast<T*>(s_raw + size_t(tile) * stride * 8);
     auto ready = [&] {
         if (threadIdx.x < nt) {
             const int t = threadIdx.x, seq = p.plan.row_seq[n0 + t], pos = p.plan.row_pos[n0 + t];
-            int slot = -1;
+            int row = -1;
             if (seq >= 0) {
                 const int page = p.table[int64_t(seq) * p.max_pages + (pos >> p.log_page)];
                 if (static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages))
-                    slot = (page << p.log_page) + (pos & ((1 << p.log_page) - 1));
+                    row = ((page * kv) << p.log_page) + (pos & ((1 << p.log_page) - 1));
                 else
                     atomicOr(p.status, kStatusBadCache);
             }
-            sl.seq[t] = seq;
-            sl.slot[t] = slot;
+            sl.live[t] = seq >= 0;
+            sl.row[t] = row;
         }
         for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
             const int t = i / half, f = i - t * half;
-            s_cs[i] = turn_of(p.plan.row_pos[n0 + t], p.freqs[f], p.amp, false);
+            s_cs[t * stride + cs_at(f, half)] = turn_of(p.plan.row_pos[n0 + t], p.freqs[f], p.amp, false);
         }
         __syncthreads();
     };
-    const int kv = p.heads[0];
-    // item or value i: a row (head of k, v or q, and token) and the place in it
-    auto place = [&](int i, int& w, int& h, int& t, int& it) {
-        const int row = p.per.div(i);
-        it = i - row * per;
-        h = p.tile.div(row);
-        t = row - h * tile;
-        w = h < kv ? 0 : h < 2 * kv ? 1 : 2;
-        h -= w * kv;
-    };
-    auto from = [&](int w, int h, int t) {
-        return static_cast<const T*>(p.x[w]) + (n0 + t) * p.xs[w][0] + h * p.xs[w][1];
-    };
-    // where a row goes: q to its dense row, k and v to the cache (or to shared memory, to be
-    // quantised) and, if asked for, to a dense row too
-    auto to = [&](int w, int h, int t, T*(&dst)[2]) {
+    // kVec: thread i has item i % per of token i / per % tile, and every step-th head; else value by value
+    const int rest = kVec ? threadIdx.x / p.per : threadIdx.x >> p.log_tile;
+    const int t = kVec ? rest & (tile - 1) : threadIdx.x & (tile - 1);
+    bool live = false;  // a row behind the last sequence stays as it was
+    int row = -1;
+    // Where head h of w (k, v, q) goes: q to its dense row, k and v to the cache (or to shared memory,
+    // to be quantised) and, if asked for, to a dense row too.
+    auto to = [&](int w, int h, T*(&dst)[2]) {
         dst[0] = dst[1] = nullptr;
-        if (w == 2) {
-            dst[0] = static_cast<T*>(p.y[2]) + (n0 + t) * p.ys[2][0] + h * p.ys[2][1];
-        } else if (kBits == 4) {
-            dst[0] = s_row + (size_t(w * kv + h) * tile + t) * p.d;
-        } else {
-            if (sl.slot[t] >= 0)
-                dst[0] = reinterpret_cast<T*>(p.cache[w]) + kv_cache_row(sl.slot[t], p.log_page, kv, h) * p.d;
-            if (p.y[w]) dst[1] = static_cast<T*>(p.y[w]) + (n0 + t) * p.ys[w][0] + h * p.ys[w][1];
+        if ((w == 2 || kBits == 16) && p.y[w])
+            dst[1] = static_cast<T*>(p.y[w]) + int64_t(n0 + t) * p.yt[w] + int64_t(h) * p.yh[w];
+        if (w < 2) {
+            if (kBits == 4) dst[0] = s_row + (((w * kv + h) << p.log_tile) + t) * p.d;
+            else if (row >= 0) dst[0] = reinterpret_cast<T*>(p.cache[w]) + int64_t(row + (h << p.log_page)) * p.d;
         }
     };
-    const int n = (2 * kv + p.heads[2]) * tile * per;
     if constexpr (kVec) {
-        move_items<T>(
-            n,
-            [&](int i, int& e0, int& e1) -> const T* {
-                int w, h, t, it;
-                place(i, w, h, t, it);
-                item_at(it, w == 1 ? 0 : p.rot, p.inter, e0, e1);
-                return t < nt ? from(w, h, t) : nullptr;
-            },
-            ready,
-            [&](int i, int e0, int e1, float(&u)[8], float(&v)[8]) {
-                int w, h, t, it;
-                place(i, w, h, t, it);
-                if (sl.seq[t] < 0) return;  // a row behind the last sequence stays as it was
-                turn_item(u, v, e0, e1, w == 1 ? 0 : p.rot, p.inter, s_cs + t * half);
-                T* dst[2];
-                to(w, h, t, dst);
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (dst[k]) {
-                        RowIo<T>::store8(dst[k] + e0, u);
-                        RowIo<T>::store8(dst[k] + e1, v);
+        const int group = rest >> p.log_tile, it = threadIdx.x - rest * p.per, step = (kRotThreads / p.per) >> p.log_tile;
+        int e0, e1;
+        item_at(it, p.rot, p.inter, e0, e1);
+        float2 cs[8];
+#pragma unroll 1
+        for (int w = 0; w < 3; ++w) {
+            if (p.heads[w] == 0) continue;
+            move_rows<T>(
+                static_cast<const T*>(p.x[w]) + int64_t(n0 + t) * p.xt[w], p.xh[w],
+                group < step && t < nt ? group : p.heads[w], step, p.heads[w], e0, e1,
+                [&] {
+                    if (w > 0) return;  // there are always keys
+                    ready();
+                    if (t < nt) {
+                        live = sl.live[t];
+                        row = sl.row[t];
+                        if (16 * it < p.rot) load_cs(cs, s_cs + t * stride, it, half);
                     }
-            });
+                },
+                [&](int h, float(&u)[8], float(&v)[8]) {
+                    if (!live) return;
+                    if (w != 1) turn_item(u, v, it, p.rot, p.inter, cs);
+                    T* dst[2];
+                    to(w, h, dst);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (dst[k]) {
+                            RowIo<T>::store8(dst[k] + e0, u);
+                            RowIo<T>::store8(dst[k] + e1, v);
+                        }
+                });
+        }
     } else {
         ready();
-        for (int i = threadIdx.x; i < n; i += kRotThreads) {
-            int w, h, t, it;
-            place(i, w, h, t, it);
-            if (t >= nt || sl.seq[t] < 0) continue;
-            const T* x = from(w, h, t);
-            const float v = turn_one([&](int e) { return RowIo<T>::load(x + e); }, it, w == 1 ? 0 : p.rot, p.inter,
-                                     s_cs + t * half);
-            T* dst[2];
-            to(w, h, t, dst);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (dst[k]) RowIo<T>::store(dst[k] + it, v);
+        if (t < nt) {
+            live = sl.live[t];
+            row = sl.row[t];
         }
+        for (int w = 0; w < 3; ++w)
+            for (int i = rest; live && i < p.heads[w] * p.per; i += kRotThreads >> p.log_tile) {
+                const int h = i / p.per, e = i - h * p.per;
+                const T* x = static_cast<const T*>(p.x[w]) + int64_t(n0 + t) * p.xt[w] + int64_t(h) * p.xh[w];
+                const float v = turn_one([&](int f) { return RowIo<T>::load(x + f); }, e, w == 1 ? 0 : p.rot, half,
+                                         p.inter, s_cs + t * stride);
+                T* dst[2];
+                to(w, h, dst);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (dst[k]) RowIo<T>::store(dst[k] + e, v);
+            }
     }
     if constexpr (kBits == 4) {
         __syncthreads();
-        const int groups = p.d / 32, log_chunks = p.d == 64 ? 3 : 4;
-        const int m = (2 * kv * tile) << log_chunks;  // a multiple of 8
-        for (int i0 = 0; i0 < m; i0 += kRotThreads) {
-            const int i = i0 + threadIdx.x, row = i >> log_chunks, ch = i & ((1 << log_chunks) - 1);
-            const int hh = p.tile.div(row), t = row - hh * tile, w = hh < kv ? 0 : 1, h = hh - w * kv;
-            const bool live = i < m && t < nt && sl.seq[t] >= 0;
-            float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (live) RowIo<T>::widen(reinterpret_cast<const uint4*>(s_row + size_t(row) * p.d + 8 * ch), u);
-            const bool on = live && sl.slot[t] >= 0;
-            const int64_t r = on ? kv_cache_row(sl.slot[t], p.log_page, kv, h) : 0;
-            float scale, mid;
-            uint32_t codes;
-            quantise8(u, w == 0, on, ch & 3, ch >> 2, groups, p.cache[w & 1] + r * (p.d / 2),
-                      p.par[w & 1] + r * (4 * groups), scale, mid, codes);
-            if (live && p.y[w]) {
-                T* y = static_cast<T*>(p.y[w]) + (n0 + t) * p.ys[w][0] + h * p.ys[w][1] + 8 * ch;
+        const int groups = p.d / 32, log_chunks = p.d == 64 ? 3 : 4, ch = threadIdx.x & ((1 << log_chunks) - 1);
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+            const int rows = kv << p.log_tile;  // a warp has whole rows: 8 or 16 lanes each
+            for (int i0 = 0; i0 < rows; i0 += kRotThreads >> log_chunks) {
+                const int i = i0 + (threadIdx.x >> log_chunks), a = i & (tile - 1), h = i >> p.log_tile;
+                const bool mine = i < rows && a < nt && sl.live[a];
+                const uint4 raw = mine ? *reinterpret_cast<const uint4*>(s_row + (w * rows + i) * p.d + 8 * ch)
+                                       : make_uint4(0, 0, 0, 0);
+                const int r = mine ? sl.row[a] : -1;
+                const int64_t at = r < 0 ? 0 : r + (h << p.log_page);
+                float scale, mid, c8[8];
+                quantise8<T>(raw, w == 0, r >= 0, ch & 3, ch >> 2, groups, p.cache[w] + at * (p.d / 2),
+                             p.par[w] + at * (4 * groups), scale, mid, c8);
+                if (mine && p.y[w]) {
+                    T* y = static_cast<T*>(p.y[w]) + int64_t(n0 + a) * p.yt[w] + int64_t(h) * p.yh[w] + 8 * ch;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) u[k] = fmaf(scale, float((codes >> (4 * k)) & 15u) - 8.f, mid);
-                if constexpr (kVec) RowIo<T>::store8(y, u);
-                else
+                    for (int k = 0; k < 8; ++k) c8[k] = fmaf(scale, c8[k], mid);
+                    if constexpr (kVec) RowIo<T>::store8(y, c8);
+                    else
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) RowIo<T>::store(y + k, u[k]);
+                        for (int k = 0; k < 8; ++k) RowIo<T>::store(y + k, c8[k]);
+                }
             }
         }
     }

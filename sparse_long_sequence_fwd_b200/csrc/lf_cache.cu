@@ -29,7 +29,6 @@ int kv_grid(int d, int bits, int gs) { return 148 * kv_ctas_per_sm(d, bits, gs >
 static_assert(148 * 4 <= kKvMaxCtas, "");
 constexpr int kMaxRotHeads = 1024;
 constexpr int kAppendSmem = 100 * 1024;
-constexpr int kAppendTileSmem = 40 * 1024;  // staged rows of a tile of more than one token
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t size_of(lf_dtype t) { return t == LF_F32 ? 4 : 2; }
@@ -71,12 +70,19 @@ bool by_eight(const void* p, int dims, const int64_t* s, size_t es) {
     return true;
 }
 
-// Tokens per CTA: as many as a CTA's threads hold at once, but no fewer CTAs than two per SM.
-int tile_for(int64_t tokens, int items_per_token, size_t element) {
-    const int64_t held = int64_t(kRotThreads) * (8 / int(element)), spread = (tokens + 295) / 296;
-    return static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>({int64_t(kRotMaxTile), held / std::max(1, items_per_token), spread})));
+// Tokens per CTA (a power of two): as many as leave a thread about five heads'
+// 16 values, so that the sines are few beside them, and no fewer CTAs than
+// two per SM.  (4096 tokens of 36 rows of 64: 4 tokens, 1024 CTAs; half or
+// twice as many heads a thread took 10.5 and 10.6 us against 8.5.)
+int log_tile_for(int64_t tokens, int heads, int per) {
+    int n = 0;
+    while ((2 << n) <= kRotMaxTile && (2 << n) * per <= kRotThreads &&
+           int64_t(2 << n) * per * heads <= int64_t(kRotThreads) * 5 && tokens >= int64_t(2 << n) * 296)
+        ++n;
+    return n;
 }
+
+bool small(const int64_t* s) { return s[0] <= INT32_MAX && s[1] <= INT32_MAX; }
 
 template <typename Tin, typename Tout>
 void launch_rotary(const RotaryParams& p, bool vec, dim3 grid, size_t smem, cudaStream_t s) {
@@ -218,8 +224,13 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
         vec = vec && by_eight(x[a], 3, xs, ei) && by_eight(y[a], 3, ys, eo);
         p.x[a] = x[a];
         p.y[a] = y[a];
-        std::copy(xs, xs + 3, p.xs[a]);
-        std::copy(ys, ys + 3, p.ys[a]);
+        if (!small(xs + 1) || !small(ys + 1)) return LF_ERR_UNSUPPORTED;
+        p.xb[a] = xs[0];
+        p.yb[a] = ys[0];
+        p.xh[a] = static_cast<int>(xs[1]);
+        p.yh[a] = static_cast<int>(ys[1]);
+        p.xt[a] = static_cast<int>(xs[2]);
+        p.yt[a] = static_cast<int>(ys[2]);
     }
     for (const Span& a : in)
         for (const Span& b : out)
@@ -238,11 +249,10 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
     p.inter = interleaved ? 1 : 0;
     p.back = inverse ? 1 : 0;
     p.amp = amplitude;
-    p.per = small_div(vec ? d / 16 : d);
-    const int tile = tile_for(int64_t(B) * T, heads * p.per.by, ei);
-    p.tile = small_div(tile);
-    const dim3 grid((T + tile - 1) / tile, B);
-    const size_t smem = size_t(tile) * (rot / 2) * sizeof(float2);
+    p.per = vec ? d / 16 : d;
+    p.log_tile = log_tile_for(int64_t(B) * T, heads, p.per);
+    const dim3 grid((T + (1 << p.log_tile) - 1) >> p.log_tile, B);
+    const size_t smem = (size_t(cs_stride(rot / 2)) << p.log_tile) * sizeof(float2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (in_dtype == LF_F32 && out_dtype == LF_F32) launch_rotary<float, float>(p, vec, grid, smem, s);
     else if (in_dtype == LF_F32 && out_dtype == LF_BF16) launch_rotary<float, __nv_bfloat16>(p, vec, grid, smem, s);
@@ -305,17 +315,21 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
         const int64_t* ys = strides + 6 + 2 * a;
         if (x[a]) {
             if (!aligned(x[a], 2) || !span_of(x[a], 2, n, xs, d, 2, &in[a])) return LF_ERR_INVALID_ARG;
+            if (!small(xs)) return LF_ERR_UNSUPPORTED;
+            p.xt[a] = static_cast<int>(xs[0]);
+            p.xh[a] = static_cast<int>(xs[1]);
             vec = vec && by_eight(x[a], 2, xs, 2);
         }
         if (y[a]) {
             if (!aligned(y[a], 2) || !span_of(y[a], 2, n, ys, d, 2, &out[a]) || !distinct(2, n, ys))
                 return LF_ERR_INVALID_ARG;
+            if (!small(ys)) return LF_ERR_UNSUPPORTED;
+            p.yt[a] = static_cast<int>(ys[0]);
+            p.yh[a] = static_cast<int>(ys[1]);
             vec = vec && by_eight(y[a], 2, ys, 2);
         }
         p.x[a] = x[a];
         p.y[a] = y[a];
-        std::copy(xs, xs + 2, p.xs[a]);
-        std::copy(ys, ys + 2, p.ys[a]);
     }
     for (const Span& a : in)
         for (const Span& b : out)
@@ -340,13 +354,11 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     p.inter = interleaved ? 1 : 0;
     p.amp = amplitude;
     p.sig = sh.sig_rows;
-    p.per = small_div(vec ? d / 16 : d);
-    int tile = tile_for(n_tokens, (2 * kv_heads + p.heads[2]) * p.per.by, 2);
+    p.per = vec ? d / 16 : d;
+    p.log_tile = log_tile_for(n_tokens, 2 * kv_heads + p.heads[2], p.per);
     const size_t staged = bits == 4 ? size_t(2) * kv_heads * d * 2 : 0;  // per token
-    while (tile > 1 && staged * tile > size_t(kAppendTileSmem)) --tile;
-    p.tile = small_div(tile);
-    const size_t smem = ((size_t(tile) * (rot / 2) * sizeof(float2) + 15) & ~size_t(15)) + staged * tile;
-    const unsigned grid = (n_tokens + tile - 1) / tile;
+    const size_t smem = (size_t(cs_stride(rot / 2)) * sizeof(float2) + staged) << p.log_tile;
+    const unsigned grid = (n_tokens + (1 << p.log_tile) - 1) >> p.log_tile;
     void (*kern)(KvAppendParams);
     if (dtype == LF_F16)
         kern = bits == 16 ? (vec ? kv_append_kernel<__half, 16, true> : kv_append_kernel<__half, 16, false>)

@@ -14,35 +14,30 @@
 // from there.  The products are in 32 bits and rounded once, on store.
 //
 // Bound: bytes.  A value is read once and written once against 3 flops, so
-// the kernels are copies that must not be slowed down by the trigonometry.
-// A CTA takes a few tokens over all heads: the sines of a token are computed
-// once into shared memory and serve its q and k heads (36 rows a token at
-// 12 heads).  A thread moves items of 16 values (two 8-value chunks that are
-// turned against each other); the loads of a CTA's first 1024 items (512 from
-// fp32), which is all of them where a token has no more, are in flight before
-// the sines are computed, so the two overlap.
+// the kernels are copies that must not be slowed down by the trigonometry or
+// by addresses.  A CTA takes a few tokens over all heads.  A thread has one
+// place in the rows of one token (16 values: two 8-value chunks that are
+// turned against each other) and takes it in every so-many-th head, so its
+// eight (cos, sin) are read once, and a head costs an address and two wide
+// loads and stores.  Its first kRotItems heads' loads are under way while the
+// CTA computes the sines (one per thread, for all heads), into shared memory
+// in an order in which a warp's reads meet every bank once.
 #pragma once
 #include "lf_common.cuh"
 #include "ptx.cuh"
 
 namespace lf {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 128;
 constexpr int kRotMaxD = 256;
 constexpr int kRotMaxTile = 16;   // tokens per CTA
 
-// 16-value items that a thread holds at once: 128 bytes of either type.
+// Heads whose 16 values a thread holds at once: 64 bytes of either type.  Few,
+// so that 72 registers do and an SM holds seven CTAs (4096 tokens of 36 rows
+// of 64, bf16: 8.3 us; six CTAs 9.2, eight, which spill, 11.2).
 template <typename T>
-constexpr int kRotItems = 8 / int(sizeof(T));
-
-// x / by for x < 2^20 and by <= 256: magic = ceil(2^32 / by), unused for 1.
-struct SmallDiv {
-    uint32_t by, magic;
-    __device__ __forceinline__ int div(int x) const { return by == 1 ? x : int(__umulhi(uint32_t(x), magic)); }
-};
-inline SmallDiv small_div(int by) {
-    return SmallDiv{uint32_t(by), by == 1 ? 0u : uint32_t((0x100000000ull + by - 1) / by)};
-}
+constexpr int kRotItems = 4 / int(sizeof(T));
+constexpr int kRotCtas = 7;
 
 // Eight values as loaded (kU 16-byte words), widened, and stored.
 template <typename T>
@@ -129,22 +124,34 @@ __device__ __forceinline__ void item_at(int it, int rot, bool inter, int& e0, in
     e1 = split ? 8 * it + rot / 2 : 16 * it + 8;
 }
 
-// Turns an item; cs: the token's rot/2 (cos, sin) in shared memory.
-__device__ __forceinline__ void turn_item(float (&a)[8], float (&b)[8], int e0, int e1, int rot, bool inter,
-                                          const float2* cs) {
+// A token's (cos, sin) in shared memory: pair f is at cs_at(f, half).  An
+// item's eight pairs 8 i .. 8 i + 7 are four 16-byte words, word j of all
+// items beside each other, and the next token's are 64 bytes further into the
+// banks (half a row of 128), so that the words j of two tokens' four items,
+// which eight lanes read together, are in different banks.
+__host__ __device__ constexpr int cs_items(int half) { return (half + 7) / 8; }
+__host__ __device__ constexpr int cs_stride(int half) {  // float2 per token
+    return 8 * cs_items(half) + ((8 * cs_items(half)) % 16 == 0 ? 8 : 0);
+}
+__device__ __forceinline__ int cs_at(int f, int half) { return 2 * (((f & 7) >> 1) * cs_items(half) + (f >> 3)) + (f & 1); }
+
+// Turns item `it` of a row with its eight pairs' cs (unused where all of
+// the item's values are copied).
+__device__ __forceinline__ void turn_item(float (&a)[8], float (&b)[8], int it, int rot, bool inter,
+                                          const float2 (&cs)[8]) {
     if (!inter) {
-        if (e0 < rot) {
+        if (16 * it < rot) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], cs[e0 + i]);
+            for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], cs[i]);
         }
     } else {
-        if (e0 < rot) {
+        if (16 * it < rot) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) turn_pair(a[2 * i], a[2 * i + 1], cs[e0 / 2 + i]);
+            for (int i = 0; i < 4; ++i) turn_pair(a[2 * i], a[2 * i + 1], cs[i]);
         }
-        if (e1 < rot) {
+        if (16 * it + 8 < rot) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) turn_pair(b[2 * i], b[2 * i + 1], cs[e1 / 2 + i]);
+            for (int i = 0; i < 4; ++i) turn_pair(b[2 * i], b[2 * i + 1], cs[4 + i]);
         }
     }
 }
@@ -152,48 +159,60 @@ __device__ __forceinline__ void turn_item(float (&a)[8], float (&b)[8], int e0, 
 // Value e of a row whose value f is at(f), turned (the element-wise path:
 // head dimensions, rot or strides that the 16-value items do not divide).
 template <typename At>
-__device__ __forceinline__ float turn_one(At at, int e, int rot, bool inter, const float2* cs) {
+__device__ __forceinline__ float turn_one(At at, int e, int rot, int half, bool inter, const float2* cs) {
     const float x = at(e);
     if (e >= rot) return x;
-    const int h = rot / 2;
-    const bool first = inter ? !(e & 1) : e < h;
-    const int i = inter ? e >> 1 : (first ? e : e - h);
-    const float y = at(inter ? e ^ 1 : (first ? e + h : e - h));
-    return first ? x * cs[i].x - y * cs[i].y : x * cs[i].x + y * cs[i].y;
+    const bool first = inter ? !(e & 1) : e < half;
+    const float2 c = cs[cs_at(inter ? e >> 1 : (first ? e : e - half), half)];
+    const float y = at(inter ? e ^ 1 : (first ? e + half : e - half));
+    return first ? x * c.x - y * c.y : x * c.x + y * c.y;
 }
 
-// A CTA's items 0 .. n-1, a thread's share of kRotItems at a time: source(i,
-// e0, e1) gives the row and the two chunks' places in it (null: no such
-// item), sink(i, e0, e1, u, v) takes the widened chunks.  ready() runs once,
-// when the first loads are under way.
-template <typename T, typename Source, typename Ready, typename Sink>
-__device__ __forceinline__ void move_items(int n, Source source, Ready ready, Sink sink) {
+// A thread's item (16 values at e0 and e1 of a row) of heads first, first +
+// step, .. below `heads`; head h's row is at x + h * stride.  ready() runs
+// when the first loads are under way, sink(h, u, v) takes the widened chunks.
+template <typename T, typename Ready, typename Sink>
+__device__ __forceinline__ void move_rows(const T* x, int stride, int first, int step, int heads, int e0, int e1,
+                                          Ready ready, Sink sink) {
     constexpr int kItems = kRotItems<T>, kU = RowIo<T>::kU;
-    for (int i0 = 0; i0 < n; i0 += kItems * kRotThreads) {
+    bool fresh = true;
+    do {
         uint4 raw[kItems][2][kU];
-        int e0[kItems], e1[kItems];
-        bool there[kItems];
 #pragma unroll
         for (int a = 0; a < kItems; ++a) {
-            const int i = i0 + a * kRotThreads + threadIdx.x;
-            const T* x = i < n ? source(i, e0[a], e1[a]) : nullptr;
-            there[a] = x != nullptr;
-            if (there[a])
+            const int h = first + a * step;
+            if (h < heads) {
+                const T* row = x + int64_t(h) * stride;
 #pragma unroll
                 for (int w = 0; w < kU; ++w) {
-                    raw[a][0][w] = __ldcs(reinterpret_cast<const uint4*>(x + e0[a]) + w);
-                    raw[a][1][w] = __ldcs(reinterpret_cast<const uint4*>(x + e1[a]) + w);
+                    raw[a][0][w] = __ldcs(reinterpret_cast<const uint4*>(row + e0) + w);
+                    raw[a][1][w] = __ldcs(reinterpret_cast<const uint4*>(row + e1) + w);
                 }
+            }
         }
-        if (i0 == 0) ready();
+        if (fresh) ready();
+        fresh = false;
 #pragma unroll
-        for (int a = 0; a < kItems; ++a)
-            if (there[a]) {
+        for (int a = 0; a < kItems; ++a) {
+            const int h = first + a * step;
+            if (h < heads) {
                 float u[8], v[8];
                 RowIo<T>::widen(raw[a][0], u);
                 RowIo<T>::widen(raw[a][1], v);
-                sink(i0 + a * kRotThreads + threadIdx.x, e0[a], e1[a], u, v);
+                sink(h, u, v);
             }
+        }
+        first += kItems * step;
+    } while (first < heads);
+}
+
+// The eight pairs of an item, from a token's row of the table.
+__device__ __forceinline__ void load_cs(float2 (&cs)[8], const float2* row, int it, int half) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 c = *reinterpret_cast<const float4*>(row + 2 * (j * cs_items(half) + it));
+        cs[2 * j] = make_float2(c.x, c.y);
+        cs[2 * j + 1] = make_float2(c.z, c.w);
     }
 }
 
@@ -202,82 +221,75 @@ __device__ __forceinline__ void move_items(int n, Source source, Ready ready, Si
 struct RotaryParams {
     const void* x[3];  // q, k, v: logical [B, heads, T, d], strides in elements
     void* y[3];
-    int64_t xs[3][3];  // (b, h, t)
-    int64_t ys[3][3];
+    int64_t xb[3], yb[3];  // sample
+    int xh[3], xt[3];      // head, token
+    int yh[3], yt[3];
     int heads[3];      // 0: absent
     const int32_t* pos;  // [B][T] (stride pos_stride, 0: shared), or null: 0 .. T-1
     int64_t pos_stride;
     const double* freqs;
     int B, T, d, rot;
-    SmallDiv tile, per;  // tokens per CTA; items (kVec) or values per row
+    int log_tile, per;  // tokens per CTA; items (kVec) or values per row
     int inter, back;
     float amp;
 };
 
 // grid: (tiles of tokens, B)
 template <typename Tin, typename Tout, bool kVec>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
-    extern __shared__ float2 s_cs[];  // [tile][rot/2]
-    const int b = blockIdx.y, tile = p.tile.by, per = p.per.by, t0 = blockIdx.x * tile;
-    const int nt = min(tile, p.T - t0), half = p.rot / 2;
+__global__ void __launch_bounds__(kRotThreads, kRotCtas) rotary_kernel(const __grid_constant__ RotaryParams p) {
+    extern __shared__ __align__(16) float2 s_cs[];  // [tile][cs_stride]
+    const int b = blockIdx.y, tile = 1 << p.log_tile, t0 = blockIdx.x * tile;
+    const int nt = min(tile, p.T - t0), half = p.rot / 2, stride = cs_stride(half);
     auto ready = [&] {
         for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
             const int t = i / half, f = i - t * half;
             const int pos = p.pos ? p.pos[b * p.pos_stride + t0 + t] : t0 + t;
-            s_cs[i] = turn_of(pos, p.freqs[f], p.amp, p.back);
+            s_cs[t * stride + cs_at(f, half)] = turn_of(pos, p.freqs[f], p.amp, p.back);
         }
         __syncthreads();
     };
-    // item or value i: a row (head of q, k or v, and token) and the place in it
-    auto place = [&](int i, int& w, int& h, int& t, int& it) {
-        const int row = p.per.div(i);
-        it = i - row * per;
-        h = p.tile.div(row);
-        t = row - h * tile;
-        w = 0;
-        if (h >= p.heads[0]) {
-            h -= p.heads[0];
-            w = 1;
-            if (h >= p.heads[1]) {
-                h -= p.heads[1];
-                w = 2;
-            }
-        }
-    };
-    auto from = [&](int w, int h, int t) {
-        return static_cast<const Tin*>(p.x[w]) + b * p.xs[w][0] + h * p.xs[w][1] + (t0 + t) * p.xs[w][2];
-    };
-    auto to = [&](int w, int h, int t) {
-        return static_cast<Tout*>(p.y[w]) + b * p.ys[w][0] + h * p.ys[w][1] + (t0 + t) * p.ys[w][2];
-    };
-    const int n = (p.heads[0] + p.heads[1] + p.heads[2]) * tile * per;
+    // kVec: thread i has item i % per of token i / per % tile, and every step-th head; else value by value
+    const int rest = kVec ? threadIdx.x / p.per : threadIdx.x >> p.log_tile;
+    const int t = kVec ? rest & (tile - 1) : threadIdx.x & (tile - 1);
     if constexpr (kVec) {
-        move_items<Tin>(
-            n,
-            [&](int i, int& e0, int& e1) -> const Tin* {
-                int w, h, t, it;
-                place(i, w, h, t, it);
-                item_at(it, w == 2 ? 0 : p.rot, p.inter, e0, e1);
-                return t < nt ? from(w, h, t) : nullptr;
-            },
-            ready,
-            [&](int i, int e0, int e1, float(&u)[8], float(&v)[8]) {
-                int w, h, t, it;
-                place(i, w, h, t, it);
-                turn_item(u, v, e0, e1, w == 2 ? 0 : p.rot, p.inter, s_cs + t * half);  // v is copied
-                Tout* y = to(w, h, t);
-                RowIo<Tout>::store8(y + e0, u);
-                RowIo<Tout>::store8(y + e1, v);
-            });
+        const int group = rest >> p.log_tile, it = threadIdx.x - rest * p.per, step = (kRotThreads / p.per) >> p.log_tile;
+        int e0, e1;
+        item_at(it, p.rot, p.inter, e0, e1);
+        float2 cs[8];
+        bool fresh = true;
+#pragma unroll 1
+        for (int w = 0; w < 3; ++w) {
+            if (p.heads[w] == 0) continue;
+            const Tin* x = static_cast<const Tin*>(p.x[w]) + b * p.xb[w] + int64_t(t0 + t) * p.xt[w];
+            Tout* y = static_cast<Tout*>(p.y[w]) + b * p.yb[w] + int64_t(t0 + t) * p.yt[w];
+            const int yh = p.yh[w];
+            move_rows<Tin>(
+                x, p.xh[w], group < step && t < nt ? group : p.heads[w], step, p.heads[w], e0, e1,
+                [&] {
+                    if (!fresh) return;
+                    fresh = false;
+                    ready();
+                    if (16 * it < p.rot && t < nt) load_cs(cs, s_cs + t * stride, it, half);
+                },
+                [&](int h, float(&u)[8], float(&v)[8]) {
+                    if (w < 2) turn_item(u, v, it, p.rot, p.inter, cs);  // v is copied
+                    Tout* row = y + int64_t(h) * yh;
+                    RowIo<Tout>::store8(row + e0, u);
+                    RowIo<Tout>::store8(row + e1, v);
+                });
+        }
     } else {
         ready();
-        for (int i = threadIdx.x; i < n; i += kRotThreads) {
-            int w, h, t, it;
-            place(i, w, h, t, it);
-            if (t >= nt) continue;
-            const Tin* x = from(w, h, t);
-            RowIo<Tout>::store(to(w, h, t) + it, turn_one([&](int e) { return RowIo<Tin>::load(x + e); }, it,
-                                                          w == 2 ? 0 : p.rot, p.inter, s_cs + t * half));
+        for (int w = 0; w < 3; ++w) {
+            const Tin* x = static_cast<const Tin*>(p.x[w]) + b * p.xb[w] + int64_t(t0 + t) * p.xt[w];
+            Tout* y = static_cast<Tout*>(p.y[w]) + b * p.yb[w] + int64_t(t0 + t) * p.yt[w];
+            for (int i = rest; t < nt && i < p.heads[w] * p.per; i += kRotThreads >> p.log_tile) {
+                const int h = i / p.per, e = i - h * p.per;
+                const Tin* row = x + int64_t(h) * p.xh[w];
+                RowIo<Tout>::store(y + int64_t(h) * p.yh[w] + e,
+                                   turn_one([&](int f) { return RowIo<Tin>::load(row + f); }, e, w == 2 ? 0 : p.rot, half,
+                                            p.inter, s_cs + t * stride));
+            }
         }
     }
 }
