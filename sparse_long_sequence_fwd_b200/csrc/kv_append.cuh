@@ -122,7 +122,8 @@ __device__ __forceinline__ void quantise8(uint4 raw, bool is_k, bool on, int cc,
             uint32_t(__half_as_ushort(hs)) | uint32_t(__half_as_ushort(hm)) << 16;
 }
 
-// grid: tiles of tokens.  smem: (cos, sin) [tile][cs_stride]; 4 bits: the
+// grid: (tiles of tokens, 1 or 3): with 3 a CTA takes k, v or q only, where
+// tiles alone are too few to fill the GPU.  smem: (cos, sin) [tile][cs_stride]; 4 bits: the
 // turned k and v rows [k heads + v heads][tile][d] in 16 bits.
 template <typename T, int kBits, bool kVec>
 __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
     const int nt = min(tile, p.N - n0), half = p.rot / 2, stride = cs_stride(half), kv = p.heads[0];
     float2* s_cs = reinterpret_cast<float2*>(s_raw);
     T* s_row = reinterpret_cast<T*>(s_raw + size_t(tile) * stride * 8);
+    const int w0 = gridDim.y == 1 ? 0 : blockIdx.y, w1 = gridDim.y == 1 ? 3 : w0 + 1;
     auto ready = [&] {
         if (threadIdx.x < nt) {
             const int t = threadIdx.x, seq = p.plan.row_seq[n0 + t], pos = p.plan.row_pos[n0 + t];
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
             sl.live[t] = seq >= 0;
             sl.row[t] = row;
         }
-        for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
+        for (int i = threadIdx.x; w0 != 1 && i < nt * half; i += kRotThreads) {
             const int t = i / half, f = i - t * half;
             s_cs[t * stride + cs_at(f, half)] = turn_of(p.plan.row_pos[n0 + t], p.freqs[f], p.amp, false);
         }
@@ -178,13 +180,13 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
         item_at(it, p.rot, p.inter, e0, e1);
         float2 cs[8];
 #pragma unroll 1
-        for (int w = 0; w < 3; ++w) {
+        for (int w = w0; w < w1; ++w) {
             if (p.heads[w] == 0) continue;
             move_rows<T>(
                 static_cast<const T*>(p.x[w]) + int64_t(n0 + t) * p.xt[w], p.xh[w],
                 group < step && t < nt ? group : p.heads[w], step, p.heads[w], e0, e1,
                 [&] {
-                    if (w > 0) return;  // there are always keys
+                    if (w > w0) return;  // there are always keys
                     ready();
                     if (t < nt) {
                         live = sl.live[t];
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
             live = sl.live[t];
             row = sl.row[t];
         }
-        for (int w = 0; w < 3; ++w)
+        for (int w = w0; w < w1; ++w)
             for (int i = rest; live && i < p.heads[w] * p.per; i += kRotThreads >> p.log_tile) {
                 const int h = i / p.per, e = i - h * p.per;
                 const T* x = static_cast<const T*>(p.x[w]) + int64_t(n0 + t) * p.xt[w] + int64_t(h) * p.xh[w];
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
         __syncthreads();
         const int groups = p.d / 32, log_chunks = p.d == 64 ? 3 : 4, ch = threadIdx.x & ((1 << log_chunks) - 1);
 #pragma unroll 1
-        for (int w = 0; w < 2; ++w) {
+        for (int w = w0; w < min(w1, 2); ++w) {
             const int rows = kv << p.log_tile;  // a warp has whole rows: 8 or 16 lanes each
             for (int i0 = 0; i0 < rows; i0 += kRotThreads >> log_chunks) {
                 const int i = i0 + (threadIdx.x >> log_chunks), a = i & (tile - 1), h = i >> p.log_tile;

@@ -35,9 +35,12 @@
 // P scale may fall out of f16's range and bf16 alone would cost more than
 // f16's output rounding, so there P scale is taken in two bf16 parts (2^-17).
 //
-// Rounding: scores, maxima, sums and O in fp32; P (at most 2^8, see below) is
-// rounded to the 16-bit type for the tensor cores, a relative error of half
-// a step per key, as the output's own rounding.
+// Rounding: scores, maxima, sums and O in fp32.  P (at most 2^8, see below)
+// goes to the tensor cores as f16 for f16 values, half a step of 2^-11 a key
+// like the output's own rounding, and in two bf16 parts (2^-15) for bf16
+// ones: the second part's MMAs are free where the bytes bound it.  Over 4
+// bits with bf16 queries P scale is one bf16, half a step of 2^-8 a key, well
+// under what the 4 bits leave of the values.
 #pragma once
 #include "kv_plan.cuh"
 #include "lf_common.cuh"
@@ -397,11 +400,21 @@ struct KvState {
         KvRegs<HD, kBits> x;
         x.load_v(sub, g, c);
         if constexpr (kBits == 16) {
-            uint32_t b[kNt][2];
+            uint32_t b[kNt][2], b2[kNt][2];
 #pragma unroll
             for (int n = 0; n < kNt; ++n) {
-                b[n][0] = movmatrix_t(pack16x2<kHalf>(s[n][0], s[n][1]));
-                b[n][1] = movmatrix_t(pack16x2<kHalf>(s[n][2], s[n][3]));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (kHalf) {
+                        b[n][i] = movmatrix_t(pack_f16x2(s[n][2 * i], s[n][2 * i + 1]));
+                    } else {  // the upper halves, and what they leave: never 0 or less, so that it times an infinite value is one
+                        const uint32_t u = __float_as_uint(s[n][2 * i]), w = __float_as_uint(s[n][2 * i + 1]);
+                        b[n][i] = movmatrix_t(__byte_perm(u, w, 0x7632));
+                        b2[n][i] = movmatrix_t(
+                            pack_bf16x2(fmaxf(s[n][2 * i] - __uint_as_float(u & 0xffff0000u), 1e-37f),
+                                        fmaxf(s[n][2 * i + 1] - __uint_as_float(w & 0xffff0000u), 1e-37f)));
+                    }
+                }
             }
 #pragma unroll
             for (int j = 0; j < HD / 64; ++j) {
@@ -414,7 +427,10 @@ struct KvState {
                     const uint32_t a0 = __byte_perm(v0[t], v1[t], 0x5410), a1 = __byte_perm(v0[t], v1[t], 0x7632);
                     const uint32_t a2 = __byte_perm(v2[t], v3[t], 0x5410), a3 = __byte_perm(v2[t], v3[t], 0x7632);
 #pragma unroll
-                    for (int n = 0; n < kNt; ++n) mma16816<kHalf>(o[n][4 * j + t], a0, a1, a2, a3, b[n][0], b[n][1]);
+                    for (int n = 0; n < kNt; ++n) {
+                        mma16816<kHalf>(o[n][4 * j + t], a0, a1, a2, a3, b[n][0], b[n][1]);
+                        if constexpr (!kHalf) mma16816<kHalf>(o[n][4 * j + t], a0, a1, a2, a3, b2[n][0], b2[n][1]);
+                    }
                 }
             }
         } else {

@@ -10,8 +10,9 @@
 // blocks [s W / G', (s + 1) W / G') of all W, so every CTA has the same number
 // of blocks, give or take one, however ragged the lengths are.  A unit that a
 // range boundary cuts leaves a partial state in every CTA that has a piece of
-// it, and a merge kernel joins them.  G' gives a CTA at least kKvMinKeys
-// keys: its start and a piece's end cost as much as a few blocks.
+// it, and a merge kernel joins them.  G' = G unless a CTA would have fewer
+// than kKvMinKeys keys: its start and a piece's end cost as much as a few
+// blocks.
 //
 // When no ordinary unit has more than kKvWholeKeys keys (a window, known on
 // the host), units stay whole: a CTA takes the units that begin in its
@@ -20,7 +21,7 @@
 //
 // Bound: latency (a few KB).  The global lists take one CTA per sequence; the
 // rows, their prefix sum and the split one CTA in all, since each needs the
-// whole of the one before.
+// whole of the one before, with what is searched held in shared memory.
 #pragma once
 #include "lf_common.cuh"
 #include "ptx.cuh"
@@ -28,10 +29,11 @@
 namespace lf {
 
 constexpr int kKvMaxGlobal = 1024;     // global tokens per sequence (the lists are ranked in O(n^2))
-constexpr int kKvMaxCtas = 2048;
+constexpr int kKvMaxCtas = 640;
 constexpr int kKvMinKeys = 256;        // keys per CTA below which fewer CTAs take part
 constexpr int kKvWholeKeys = 1024;
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqs = 4096, kPlanRows = 1024;  // up to which cu_tokens and the prefix sum are searched in shared memory
 constexpr uint32_t kStatusBadCache = 4u;  // a row or page of a cache call outside its range (left out)
 constexpr uint32_t kStatusBadPlan = 8u;   // a cache call with another plan than its arguments say
 
@@ -47,7 +49,7 @@ struct KvStart {  // where a CTA's range starts, with the row's entries
 
 struct KvPlan {  // views into the caller's plan buffer
     uint64_t* sig;       // [2]: of the rows (append), of rows and work (attention)
-    int64_t* prefix;     // [N + 1] blocks before each row
+    int64_t* prefix;     // [N] blocks before each row
     KvStart* start;      // [G]
     KvCut* cut;          // [G]
     int32_t* row_seq;    // [N], -1: the row is none (behind the last sequence, or out of range)
@@ -62,6 +64,7 @@ struct KvShape {  // what a plan is made for
     int q_heads, kv_heads, nsub, r, G;
     int block;           // keys per block
     int cut;             // 0: units stay whole
+    int one_dil;         // all heads have dil[0]
     uint64_t sig_rows, sig_all;
     int32_t dil[kMaxHeads];
 };
@@ -74,7 +77,7 @@ inline KvPlanLayout kv_plan_layout(int S, int N, int n_global) {
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     KvPlanLayout L;
     L.prefix = 256;
-    L.start = up(L.prefix + sizeof(int64_t) * (size_t(N) + 1));
+    L.start = up(L.prefix + sizeof(int64_t) * size_t(N));
     L.cut = up(L.start + sizeof(KvStart) * kKvMaxCtas);
     L.seq = up(L.cut + sizeof(KvCut) * kKvMaxCtas);
     L.pos = up(L.seq + sizeof(int32_t) * size_t(N));
@@ -154,15 +157,20 @@ __global__ void __launch_bounds__(256) kv_plan_globals_kernel(const int32_t* gid
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_t* cu, const int32_t* context,
                                                                     const __grid_constant__ KvShape sh, KvPlan p,
                                                                     uint32_t* status) {
-    __shared__ int64_t s_warp[32];
-    __shared__ int64_t s_carry;
+    __shared__ int32_t s_cu[kPlanSeqs + 1];
+    __shared__ int64_t s_prefix[kPlanRows], s_bound[kKvMaxCtas + 1], s_warp[32], s_carry;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s_carry = 0;
     for (int s = tid; s <= sh.S; s += kPlanThreads) {
         const int c = cu[s];
+        if (s <= kPlanSeqs) s_cu[s] = c;
         if (s == 0 ? c != 0 : c < cu[s - 1]) atomicOr(status, kStatusBadCache);
         if (s == sh.S && c > sh.N) atomicOr(status, kStatusBadCache);
     }
+    __syncthreads();
+    const int32_t* cus = sh.S <= kPlanSeqs ? s_cu : cu;
+    const int64_t* prefix = sh.N <= kPlanRows ? s_prefix : p.prefix;
+    auto blocks_of = [&](int pos, int ng, int h) { return KvKeys(pos, ng, sh.r, sh.dil[h]).blocks(sh.block); };
     for (int n0 = 0; n0 < sh.N; n0 += kPlanThreads) {
         const int n = n0 + tid;
         int64_t blocks = 0;
@@ -170,14 +178,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
             int lo = 0, hi = sh.S;  // the last s with cu[s] <= n
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (cu[mid] <= n) lo = mid;
+                if (cus[mid] <= n) lo = mid;
                 else hi = mid;
             }
-            const int c0 = cu[lo], c1 = cu[lo + 1];
+            const int c0 = cus[lo], c1 = cus[lo + 1];
             int seq = -1, pos = 0, ng = 0;
             if (c0 >= 0 && c0 <= n && n < c1) {
-                const int64_t at = int64_t(context[lo]) + (n - c0);
-                if (context[lo] >= 0 && at < sh.max_len) {
+                const int before = context[lo];
+                const int64_t at = int64_t(before) + (n - c0);
+                if (before >= 0 && at < sh.max_len) {
                     seq = lo;
                     pos = static_cast<int>(at);
                 } else {
@@ -196,7 +205,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
                     }
                     ng = (a < cnt && g[a] == pos) ? -1 : a;
                 }
-                for (int h = 0; h < sh.kv_heads; ++h) blocks += KvKeys(pos, ng, sh.r, sh.dil[h]).blocks(sh.block);
+                if (sh.one_dil) blocks = int64_t(sh.kv_heads) * blocks_of(pos, ng, 0);
+                else
+                    for (int h = 0; h < sh.kv_heads; ++h) blocks += blocks_of(pos, ng, h);
                 blocks *= sh.nsub;
             }
             p.row_seq[n] = seq;
@@ -222,37 +233,38 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
         }
         __syncthreads();
         const int64_t before = s_carry + (warp ? s_warp[warp - 1] : 0) + sum - blocks;
-        if (n < sh.N) p.prefix[n] = before;
+        if (n < sh.N) {
+            p.prefix[n] = before;
+            if (n < kPlanRows) s_prefix[n] = before;
+        }
         __syncthreads();
         if (tid == kPlanThreads - 1) s_carry = before + blocks;
         __syncthreads();
     }
     const int64_t W = s_carry;
     if (tid == 0) {
-        p.prefix[sh.N] = W;
         p.sig[0] = sh.sig_rows;
         p.sig[1] = sh.sig_all;
     }
-    __syncthreads();
     // The split.  Block x of the sequence: its row, unit, and place in the unit.
-    const int64_t wide = (W * sh.block + kKvMinKeys - 1) / kKvMinKeys;
+    const int64_t wide = sh.cut ? (W * sh.block + kKvMinKeys - 1) / kKvMinKeys : W;
     const int64_t G = wide < sh.G ? wide : sh.G;  // no CTA below G has an empty range
     auto locate = [&](int64_t x, KvStart& at, int64_t& unit_first, int64_t& unit_end) {
         int lo = 0, hi = sh.N;  // the last row with prefix <= x (rows without blocks are passed over)
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (p.prefix[mid] <= x) lo = mid;
+            if (prefix[mid] <= x) lo = mid;
             else hi = mid;
         }
-        int64_t left = x - p.prefix[lo];
+        int64_t left = x - prefix[lo];
         at.row = lo;
         at.seq = p.row_seq[lo];
         at.pos = p.row_pos[lo];
         at.ng = p.row_ng[lo];
         int unit = 0, nb = 1;
         for (int h = 0; h < sh.kv_heads; ++h) {
-            nb = KvKeys(at.pos, at.ng, sh.r, sh.dil[h]).blocks(sh.block);
-            const int64_t all = int64_t(nb) * sh.nsub;
+            nb = blocks_of(at.pos, at.ng, h);
+            const int64_t all = int64_t(nb) * sh.nsub * (sh.one_dil ? sh.kv_heads : 1);
             if (left < all) {
                 unit = h * sh.nsub + static_cast<int>(left / nb);
                 left %= nb;
@@ -265,34 +277,32 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
         unit_first = x - left;
         unit_end = unit_first + nb;
     };
-    // the first unit boundary at or behind block x
-    auto boundary = [&](int64_t x) {
-        if (x >= W) return W;
-        KvStart at;
-        int64_t first, end;
-        locate(x, at, first, end);
-        return first == x ? x : end;
-    };
+    for (int s = tid; s <= G; s += kPlanThreads) {  // where the CTAs' ranges start
+        int64_t x = G > 0 ? s * W / G : 0;
+        if (!sh.cut && x < W) {  // the first unit boundary at or behind x
+            KvStart at;
+            int64_t first, end;
+            locate(x, at, first, end);
+            if (first < x) x = end;
+        }
+        s_bound[s] = x;
+    }
+    __syncthreads();
     for (int s = tid; s < sh.G; s += kPlanThreads) {
         KvStart at{0, 0, 0, 0, 0, 0, 0};
         KvCut cut{0, 0, -1, 0};
-        if (s < G) {
-            int64_t x0 = s * W / G, x1 = (s + 1) * W / G, first, end;
-            if (!sh.cut) {
-                x0 = boundary(x0);
-                x1 = boundary(x1);
-            }
-            if (x0 < x1) {
-                locate(x0, at, first, end);
-                at.n = x1 - x0;
-                if (sh.cut) {
-                    KvStart last;
-                    locate(x1 - 1, last, first, end);
-                    if (first >= x0 && end > x1) {
-                        cut.row = last.row;
-                        cut.unit = last.unit;
-                        cut.last = static_cast<int>((end * G - 1) / W);  // the CTA that has block end - 1
-                    }
+        if (s < G && s_bound[s] < s_bound[s + 1]) {
+            const int64_t x0 = s_bound[s], x1 = s_bound[s + 1];
+            int64_t first, end;
+            locate(x0, at, first, end);
+            at.n = x1 - x0;
+            if (sh.cut) {
+                KvStart last;
+                locate(x1 - 1, last, first, end);
+                if (first >= x0 && end > x1) {
+                    cut.row = last.row;
+                    cut.unit = last.unit;
+                    cut.last = static_cast<int>((end * G - 1) / W);  // the CTA that has block end - 1
                 }
             }
         }

@@ -74,13 +74,18 @@ bool by_eight(const void* p, int dims, const int64_t* s, size_t es) {
 // 16 values, so that the sines are few beside them, and no fewer CTAs than
 // two per SM.  (4096 tokens of 36 rows of 64: 4 tokens, 1024 CTAs; half or
 // twice as many heads a thread took 10.5 and 10.6 us against 8.5.)
-int log_tile_for(int64_t tokens, int heads, int per) {
+// Where 4-bit rows follow through shared memory, twice as many heads (16384
+// tokens of 32 rows: 47 -> 44 us).
+int log_tile_for(int64_t tokens, int heads, int per, bool staged) {
     int n = 0;
     while ((2 << n) <= kRotMaxTile && (2 << n) * per <= kRotThreads &&
-           int64_t(2 << n) * per * heads <= int64_t(kRotThreads) * 5 && tokens >= int64_t(2 << n) * 296)
+           int64_t(2 << n) * per * heads <= int64_t(kRotThreads) * (staged ? 10 : 5) && tokens >= int64_t(2 << n) * 296)
         ++n;
     return n;
 }
+
+// CTAs for q, k and v apart, where tiles of one token are under two per SM.
+int apart(int64_t tiles) { return tiles < 296 ? 3 : 1; }
 
 bool small(const int64_t* s) { return s[0] <= INT32_MAX && s[1] <= INT32_MAX; }
 
@@ -120,7 +125,11 @@ lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_he
     const int group = q_heads / kv_heads;
     sh->nsub = (group + 15) / 16;
     sh->r = std::min(r, sh->max_len);
-    for (int h = 0; h < kv_heads; ++h) sh->dil[h] = dil ? std::min(dil[h], sh->max_len) : 1;
+    sh->one_dil = 1;
+    for (int h = 0; h < kv_heads; ++h) {
+        sh->dil[h] = dil ? std::min(dil[h], sh->max_len) : 1;
+        if (sh->dil[h] != sh->dil[0]) sh->one_dil = 0;
+    }
     // no more CTAs than blocks that ordinary rows can have
     const int64_t keys = std::min<int64_t>(int64_t(sh->r) + 1, sh->max_len);
     sh->block = kv_block(bits);
@@ -250,8 +259,9 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
     p.back = inverse ? 1 : 0;
     p.amp = amplitude;
     p.per = vec ? d / 16 : d;
-    p.log_tile = log_tile_for(int64_t(B) * T, heads, p.per);
-    const dim3 grid((T + (1 << p.log_tile) - 1) >> p.log_tile, B);
+    p.log_tile = log_tile_for(int64_t(B) * T, heads, p.per, false);
+    const unsigned tiles = (T + (1 << p.log_tile) - 1) >> p.log_tile;
+    const dim3 grid(tiles, B, apart(int64_t(tiles) * B));
     const size_t smem = (size_t(cs_stride(rot / 2)) << p.log_tile) * sizeof(float2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (in_dtype == LF_F32 && out_dtype == LF_F32) launch_rotary<float, float>(p, vec, grid, smem, s);
@@ -355,10 +365,11 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     p.amp = amplitude;
     p.sig = sh.sig_rows;
     p.per = vec ? d / 16 : d;
-    p.log_tile = log_tile_for(n_tokens, 2 * kv_heads + p.heads[2], p.per);
+    p.log_tile = log_tile_for(n_tokens, 2 * kv_heads + p.heads[2], p.per, bits == 4);
     const size_t staged = bits == 4 ? size_t(2) * kv_heads * d * 2 : 0;  // per token
     const size_t smem = (size_t(cs_stride(rot / 2)) * sizeof(float2) + staged) << p.log_tile;
-    const unsigned grid = (n_tokens + (1 << p.log_tile) - 1) >> p.log_tile;
+    const unsigned tiles = (n_tokens + (1 << p.log_tile) - 1) >> p.log_tile;
+    const dim3 grid(tiles, apart(tiles));
     void (*kern)(KvAppendParams);
     if (dtype == LF_F16)
         kern = bits == 16 ? (vec ? kv_append_kernel<__half, 16, true> : kv_append_kernel<__half, 16, false>)

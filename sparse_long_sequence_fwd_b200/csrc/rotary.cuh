@@ -234,14 +234,16 @@ struct RotaryParams {
     float amp;
 };
 
-// grid: (tiles of tokens, B)
+// grid: (tiles of tokens, B, 1 or 3): with 3 a CTA takes q, k or v only, where
+// tiles alone are too few to fill the GPU.
 template <typename Tin, typename Tout, bool kVec>
 __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotary_kernel(const __grid_constant__ RotaryParams p) {
     extern __shared__ __align__(16) float2 s_cs[];  // [tile][cs_stride]
     const int b = blockIdx.y, tile = 1 << p.log_tile, t0 = blockIdx.x * tile;
     const int nt = min(tile, p.T - t0), half = p.rot / 2, stride = cs_stride(half);
+    const int w0 = gridDim.z == 1 ? 0 : blockIdx.z, w1 = gridDim.z == 1 ? 3 : w0 + 1;
     auto ready = [&] {
-        for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
+        for (int i = threadIdx.x; w0 < 2 && i < nt * half; i += kRotThreads) {
             const int t = i / half, f = i - t * half;
             const int pos = p.pos ? p.pos[b * p.pos_stride + t0 + t] : t0 + t;
             s_cs[t * stride + cs_at(f, half)] = turn_of(pos, p.freqs[f], p.amp, p.back);
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotary_kernel(const __g
         float2 cs[8];
         bool fresh = true;
 #pragma unroll 1
-        for (int w = 0; w < 3; ++w) {
+        for (int w = w0; w < w1; ++w) {
             if (p.heads[w] == 0) continue;
             const Tin* x = static_cast<const Tin*>(p.x[w]) + b * p.xb[w] + int64_t(t0 + t) * p.xt[w];
             Tout* y = static_cast<Tout*>(p.y[w]) + b * p.yb[w] + int64_t(t0 + t) * p.yt[w];
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotary_kernel(const __g
         }
     } else {
         ready();
-        for (int w = 0; w < 3; ++w) {
+        for (int w = w0; w < w1; ++w) {
             const Tin* x = static_cast<const Tin*>(p.x[w]) + b * p.xb[w] + int64_t(t0 + t) * p.xt[w];
             Tout* y = static_cast<Tout*>(p.y[w]) + b * p.yb[w] + int64_t(t0 + t) * p.yt[w];
             for (int i = rest; t < nt && i < p.heads[w] * p.per; i += kRotThreads >> p.log_tile) {
