@@ -293,8 +293,8 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  * already holds their own keys.  q and out: DEVICE rows
  * [n_tokens][q_heads][d], strides HOST int64 [4]: (token, head) of q, of out;
  * q's rows are 16-byte aligned.  workspace: DEVICE,
- * lf_attn_cache_workspace_bytes bytes for these sizes (0 where no sequence's
- * keys are ever split between CTAs; NULL will do then), 16-byte aligned, of
+ * lf_attn_cache_workspace_bytes bytes for these sizes (0 where no row's keys
+ * are split between CTAs; NULL will do then), 16-byte aligned, of
  * this call alone while it runs.  The plan must have been made with the
  * same n_seqs, n_tokens, n_global, page, max_pages, heads, d, bits, r and dil
  * (lf_attn_cache_append: n_seqs, n_tokens, page and max_pages); a call with
@@ -312,8 +312,8 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
                                int n_pages, int page, const int32_t* table, int max_pages, const void* plan, int n_seqs,
                                int n_tokens, int n_global, int q_heads, int kv_heads, int d, const double* freqs,
                                int rot, int interleaved, float amplitude, lf_dtype dtype, int bits, void* stream);
-uint64_t lf_attn_cache_workspace_bytes(int n_global, int page, int max_pages, int q_heads, int kv_heads, int d,
-                                       int bits, int r);
+uint64_t lf_attn_cache_workspace_bytes(int n_tokens, int n_global, int page, int max_pages, int q_heads,
+                                       int kv_heads, int d, int bits, int r);
 lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, const void* k_cache, const void* v_cache,
                             const void* k_par, const void* v_par, int n_pages, int page, const int32_t* table,
                             int max_pages, const void* plan, int n_seqs, int n_tokens, int n_global, int q_heads,

@@ -14,10 +14,10 @@
 // than kKvMinKeys keys: its start and a piece's end cost as much as a few
 // blocks.
 //
-// When no ordinary unit has more than kKvWholeKeys keys (a window, known on
-// the host), units stay whole: a CTA takes the units that begin in its
-// range, and nothing is merged.  (A global row, which sees every key, is then
-// one CTA's work too.)
+// Units stay whole where cutting them would gain less than the merge costs
+// (decided on the host from the window and the number of rows): a CTA takes
+// the units that begin in its range, and nothing is merged.  (A global row,
+// which sees every key, is then one CTA's work too.)
 //
 // Bound: latency (a few KB).  The global lists take one CTA per sequence; the
 // rows, their prefix sum and the split one CTA in all, since each needs the
@@ -30,8 +30,7 @@ namespace lf {
 
 constexpr int kKvMaxGlobal = 1024;     // global tokens per sequence (the lists are ranked in O(n^2))
 constexpr int kKvMaxCtas = 640;
-constexpr int kKvMinKeys = 256;        // keys per CTA below which fewer CTAs take part
-constexpr int kKvWholeKeys = 1024;
+constexpr int kKvMinKeys = 128;        // keys per CTA below which fewer CTAs take part
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 4096, kPlanRows = 1024;  // up to which cu_tokens and the prefix sum are searched in shared memory
 constexpr uint32_t kStatusBadCache = 4u;  // a row or page of a cache call outside its range (left out)

@@ -102,6 +102,17 @@ uint64_t mix(uint64_t h, uint64_t x) {  // FNV-1a over the value's bytes
 
 int heads_of_unit(int group, int nsub) { return (group + nsub - 1) / nsub; }
 
+// Whether units (of up to `keys` keys) are cut between the CTAs.  Whole, the
+// CTAs take ceil(units / grid) rounds of them; cut, units / grid, and a merge
+// that costs about as much as kCutKeys keys (one token, 12 heads, 258 keys:
+// 6.2 us whole, 8.4 cut; 24 tokens, 2 heads, 1029 keys: 30 whole, 17 cut).
+// Long ones are always cut, since their lengths may differ.
+constexpr int64_t kCutKeys = 320, kLongKeys = 4096;
+bool cut_units(int64_t units, int64_t keys, int64_t grid) {
+    const int64_t rounds = (units + grid - 1) / grid;
+    return keys > kLongKeys || keys * (rounds * grid - units) > kCutKeys * grid;
+}
+
 lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_heads, int kv_heads, int d, int bits,
                    int r, const int32_t* dil, KvShape* sh) {
     if (S < 1 || N < 0 || n_global < 0 || page < 1 || max_pages < 1 || q_heads < 1 || kv_heads < 1 || r < 0)
@@ -133,11 +144,10 @@ lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_he
     // no more CTAs than blocks that ordinary rows can have
     const int64_t keys = std::min<int64_t>(int64_t(sh->r) + 1, sh->max_len);
     sh->block = kv_block(bits);
-    const int64_t blocks = (keys + n_global + sh->block - 1) / sh->block;
+    const int64_t blocks = (keys + n_global + sh->block - 1) / sh->block, units = int64_t(N) * kv_heads * sh->nsub;
     const int64_t grid = kv_grid(d, bits, heads_of_unit(group, sh->nsub));
-    sh->cut = blocks * sh->block > kKvWholeKeys;
-    sh->G = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(grid, blocks * std::min<int64_t>(N, grid) * kv_heads * sh->nsub)));
+    sh->cut = cut_units(units, keys + n_global, grid);
+    sh->G = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(grid, blocks * std::min(units, grid))));
     uint64_t h = 14695981039346656037ull;
     for (int64_t x : {int64_t(S), int64_t(N), int64_t(page), int64_t(max_pages)}) h = mix(h, uint64_t(x));
     sh->sig_rows = h;
@@ -381,10 +391,10 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
 }
 
-uint64_t lf_attn_cache_workspace_bytes(int n_global, int page, int max_pages, int q_heads, int kv_heads, int d,
+uint64_t lf_attn_cache_workspace_bytes(int n_tokens, int n_global, int page, int max_pages, int q_heads, int kv_heads, int d,
                                        int bits, int r) {
     KvShape sh;
-    if (kv_shape(1, 1, n_global, page, max_pages, q_heads, kv_heads, d, bits, r, nullptr, &sh) != LF_OK || !sh.cut)
+    if (kv_shape(1, n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, r, nullptr, &sh) != LF_OK || !sh.cut)
         return 0;
     const int gs = heads_of_unit(q_heads / kv_heads, sh.nsub);
     return uint64_t(2) * kv_grid(d, bits, gs) * gs * kv_piece_row(d) * sizeof(float);
@@ -406,7 +416,7 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     if (!span_of(q, 2, n, strides, d, 2, &a) || !span_of(out, 2, n, strides + 2, d, 2, &b) ||
         !distinct(2, n, strides + 2) || !by_eight(q, 2, strides, 2) || !aligned(out, 2) || a.meets(b))
         return LF_ERR_INVALID_ARG;
-    const uint64_t need = lf_attn_cache_workspace_bytes(n_global, page, max_pages, q_heads, kv_heads, d, bits, r);
+    const uint64_t need = lf_attn_cache_workspace_bytes(n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, r);
     if (need > 0 && !workspace) return LF_ERR_INVALID_ARG;
     if (workspace_bytes < need) return LF_ERR_SCRATCH_TOO_SMALL;
     if (n_tokens == 0) return LF_OK;

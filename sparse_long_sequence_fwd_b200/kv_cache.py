@@ -100,7 +100,8 @@ class Plan:
             raise LfAttnError(1, "lf_attn_cache_plan_bytes")
         self.d, self.bits = cache.d, cache.bits
         self.workspace_bytes = lf_attn.load().lf_attn_cache_workspace_bytes(
-            self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.d, self.bits, self.r)
+            self.n_tokens, self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.d, self.bits,
+            self.r)
         self.buffer = _on_stream(stream, self._inputs(),
                                  lambda raw: torch.empty(size, dtype=torch.uint8, device=context.device))
         self.refresh(stream)

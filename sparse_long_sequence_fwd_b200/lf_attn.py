@@ -83,7 +83,7 @@ def load():
         lib.lf_attn_cache_append.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, P, I, P, I, I, I, I, I, I, P, I, I,
                                              F, I, I, P]
         lib.lf_attn_cache_append.restype = I
-        lib.lf_attn_cache_workspace_bytes.argtypes = [I] * 8
+        lib.lf_attn_cache_workspace_bytes.argtypes = [I] * 9
         lib.lf_attn_cache_workspace_bytes.restype = ctypes.c_uint64
         lib.lf_attn_cache_fwd.argtypes = [P, P, P, P, P, P, P, I, I, P, I, P, I, I, I, I, I, I, I, P, F, I, I, P,
                                           ctypes.c_uint64, P]

@@ -79,11 +79,12 @@ def test_sizes(lib):
     assert lib.lf_attn_cache_plan_bytes(1, 0, 0) > 0
     for bad in ((0, 1, 0), (1, -1, 0), (1, 1, -1), (1, 1, 1025), ((1 << 20) + 1, 1, 0)):
         assert lib.lf_attn_cache_plan_bytes(*bad) == 0
-    size = lambda ng=0, page=16, mp=1000, hq=12, hkv=12, d=64, bits=16, r=1 << 30: (  # noqa: E731
-        lib.lf_attn_cache_workspace_bytes(ng, page, mp, hq, hkv, d, bits, r))
+    size = lambda n=1, ng=0, page=16, mp=1000, hq=12, hkv=12, d=64, bits=16, r=1 << 30: (  # noqa: E731
+        lib.lf_attn_cache_workspace_bytes(n, ng, page, mp, hq, hkv, d, bits, r))
     assert size() > 0 and size(hq=24) > size() and size(r=5000) > 0
     assert size(r=100) == 0 and size(mp=2) == 0        # windows, or tables, that no CTA needs help with
-    for bad in (dict(hkv=5), dict(hq=0), dict(d=96), dict(hq=256, hkv=1), dict(bits=8), dict(ng=-1)):
+    assert size(n=10000, r=1000) == 0                  # or rows enough for all
+    for bad in (dict(hkv=5), dict(hq=0), dict(d=96), dict(hq=256, hkv=1), dict(bits=8), dict(ng=-1), dict(n=-1)):
         assert size(**bad) == 0
 
 
