@@ -249,7 +249,8 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  *            (scale, mid).  With n = d / 32, a K row is 32-bit words [4][n],
  *            word [c][g] holding values 32 g + 8 c + 0..7 from its lowest
  *            four bits up; a V row is 16-bit units [8][n], unit [r][g]
- *            holding values 32 g + 4 r + 0..3.
+ *            holding values 32 g + 4 r + 0..3.  Values are in fp16's range:
+ *            the attention reads a V value as the nearest fp16.
  * dtype is LF_BF16 or LF_F16 (queries, output, dense rows), d is 64 or 128,
  * q_heads <= 128 a multiple of kv_heads, n_pages * kv_heads * page < 2^31,
  * max_pages * page <= 2^30.  Cache and par pointers are 16-byte aligned.
@@ -286,8 +287,8 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  *   rot == 0    leaves keys and queries as they are
  *   4 bits: scale = fp16((max - min) / 15), mid = fp16(min + 8 scale), c =
  *   (x - mid) / scale + 8 rounded to the nearest, ties to even (8 where scale
- *   is 0), x being the turned value in `dtype`.  A group with an infinity or a
- *   NaN, or whose scale or mid is past fp16's range, is held as NaN.
+ *   is 0), x being the turned value in `dtype`.  A group with a value past
+ *   fp16's range, an infinity or a NaN is held as NaN.
  *
  * lf_attn_cache_fwd -- the attention of the step's rows over the cache, which
  * already holds their own keys.  q and out: DEVICE rows

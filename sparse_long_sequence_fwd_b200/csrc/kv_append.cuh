@@ -6,8 +6,8 @@
 // 4 bits (groups of 32 values x of the row, in the 16-bit type):
 //   scale = fp16((max - min) / 15), mid = fp16(min + 8 scale),
 //   c = clamp(round((x - mid) / scale) + 8, 0, 15)   (ties to even; 8 if scale is 0)
-// and the group stands for mid + scale (c - 8).  A group with an infinity or
-// a NaN, or whose scale or mid is past fp16's range, is held as NaN (mid).
+// and the group stands for mid + scale (c - 8).  A group with a value past
+// fp16's range, an infinity or a NaN is held as NaN (mid).
 // Near a border between codes the subtraction and the division are IEEE ones,
 // so that the codes are the formula's.
 //
@@ -82,7 +82,7 @@ __device__ __forceinline__ void quantise8(uint4 raw, bool is_k, bool on, int cc,
     const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
     scale = __half2float(hs);
     __half hm = __float2half_rn(__fadd_rn(lo, __fmul_rn(8.f, scale)));
-    if (!(scale < INFINITY) || !(fabsf(__half2float(hm)) < INFINITY)) hm = __float2half_rn(NAN);
+    if (!(lo >= -65504.f && hi <= 65504.f)) hm = __float2half_rn(NAN);
     mid = __half2float(hm);
     const float inv = scale > 0.f ? __fdividef(1.f, 15.f * scale) : 0.f;  // scale 0: all codes 8
     constexpr float kRound = 12582912.f;

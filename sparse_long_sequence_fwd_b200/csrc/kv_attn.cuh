@@ -27,20 +27,21 @@
 // table is read one block before that, and the next unit's queries while the
 // last block of a unit is computed.
 //
-// 4 bits: a group of 32 values is mid + scale (c - 8).  Codes are exact in bf16
-// and f16, so the MMAs run on them: q . k = sum over groups of
-// scale (q . (c - 8)) + mid (sum of q), in fp32; and for the values P scale
-// takes P's place, and the P mid are summed in fp32 beside.  Bound here:
-// instructions, half of them to spread nibbles into the MMA's operands.  With f16 queries
-// P scale may fall out of f16's range and bf16 alone would cost more than
-// f16's output rounding, so there P scale is taken in two bf16 parts (2^-17).
+// 4 bits: a group of 32 values is mid + scale (c - 8).  A code or'ed into the
+// mantissa of 1024 is an f16 (1024 + c, or 1024 + 16 c for a nibble four bits
+// up), so all MMAs are f16 here.  K stays codes: q . k = sum over groups of
+// scale (sum of q (c - 8)) + mid (sum of q) in fp32, the 1024 taken off the
+// fp32 sum (what that loses is 1024 steps of 2^-24 of the q sum).  Queries are
+// brought to [-2, 2] by a power of two for it, which f16 holds exactly down to
+// 2^-14 of the largest, and to 2^-25 of it below.  V is made f16 values, one
+// rounding (2^-11).  Bound here: instructions (integer ones to spread nibbles,
+// then MMAs), not bytes.
 //
 // Rounding: scores, maxima, sums and O in fp32.  P (at most 2^8, see below)
-// goes to the tensor cores as f16 for f16 values, half a step of 2^-11 a key
-// like the output's own rounding, and in two bf16 parts (2^-15) for bf16
-// ones: the second part's MMAs are free where the bytes bound it.  Over 4
-// bits with bf16 queries P scale is one bf16, half a step of 2^-8 a key, well
-// under what the 4 bits leave of the values.
+// goes to the tensor cores as one f16 (2^-11) with f16 values, and in two bf16
+// parts (2^-15) with bf16 ones: the second part's MMAs are free where the
+// bytes bound it.  With f16 queries over 4 bits, where V is rounded too, P is
+// two f16 parts.
 #pragma once
 #include "kv_plan.cuh"
 #include "lf_common.cuh"
@@ -63,7 +64,7 @@ __host__ __device__ constexpr int kv_block(int bits) { return kKvWarps * 16 * kv
 // CTAs of four warps that an SM holds at once: by the ring's shared memory
 // (16 bits: 48 KB a CTA at d = 64, 96 KB at 128), else by registers.
 __host__ __device__ constexpr int kv_ctas_per_sm(int d, int bits, bool two) {
-    return d == 64 ? (two ? 3 : 4) : (bits == 16 || two ? 2 : 3);
+    return d == 64 ? (two || bits == 4 ? 3 : 4) : (bits == 16 || two ? 2 : 3);
 }
 
 // A stage: for each 16 keys the K rows, the V rows, and for 4 bits their parameters.
@@ -133,18 +134,18 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     return y;
 }
 
-// Four-bit codes c in bits 0-3 and 16-19 of x (others ignored) as two 16-bit
-// floats kCodeBase + c: the code or'ed into the mantissa of 2^10 (f16) or 2^7
-// (bf16).  The base is taken off again where it costs least: for K in the
-// groups' mid (mid' = mid - (base + 8) scale), for V by one more MMA with a
-// constant -(base + 8) in V's place on the same rounded P scale.  Both are
-// fp32 sums of exact products, so what that loses is 136 (1032) steps of 2^-24.
-template <bool kHalf>
-constexpr float kCodeBase = kHalf ? 1024.f : 128.f;
-constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16x2
-template <bool kHalf>
+// Two nibbles of x, bits 0-3 and 16-19 (kUp: 4-7 and 20-23), as f16 1024 + c (1024 + 16 c).
+template <bool kUp>
 __device__ __forceinline__ uint32_t code_pair(uint32_t x) {
-    return (x & 0x000f000fu) | (kHalf ? 0x64006400u : 0x43004300u);
+    return (x & (kUp ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+}
+// ... and as c - 8, exactly.
+template <bool kUp>
+__device__ __forceinline__ __half2 code_value(uint32_t x) {
+    const uint32_t y = code_pair<kUp>(x), bias = kUp ? 0xd480d480u : 0xe408e408u;  // -72, -1032
+    const __half2 b = *reinterpret_cast<const __half2*>(&bias), v = *reinterpret_cast<const __half2*>(&y);
+    if constexpr (kUp) return __hfma2(v, __float2half2_rn(0.0625f), b);
+    else return __hadd2(v, b);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {  // zeros if not there
@@ -253,7 +254,7 @@ struct KvRegs<HD, 4> {
     uint32_t k[2][kGroups];   // keys g, g + 8: word [c] of each group
     uint32_t v[4][HD / 64];   // keys 2c, ..: units [g] of two groups each
     uint32_t kp[2][kGroups];  // keys g, g + 8: (scale, mid) of each group
-    uint32_t vp[2][kGroups];
+    uint32_t vp[4][kGroups];  // keys 2c, ..
     __device__ __forceinline__ void load_k(const uint8_t* s, int g, int c) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -263,10 +264,11 @@ struct KvRegs<HD, 4> {
     }
     __device__ __forceinline__ void load_v(const uint8_t* s, int g, int c) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) load_words(vp[i], s + St::kVp + (g + 8 * i) * St::kPar);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            load_words(v[i], s + St::kV + v_place(2 * c + (i & 1) + 8 * (i >> 1)) * St::kRow + g * (2 * kGroups));
+        for (int i = 0; i < 4; ++i) {
+            const int k = 2 * c + (i & 1) + 8 * (i >> 1);
+            load_words(v[i], s + St::kV + v_place(k) * St::kRow + g * (2 * kGroups));
+            load_words(vp[i], s + St::kVp + k * St::kPar);
+        }
     }
 };
 
@@ -283,8 +285,10 @@ struct KvState {
     uint32_t q[kNt][HD / 16][2];
     float o[kNt][HD / 16][4];
     float m[kNt][2], l[kNt][2];
-    float qs[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2];  // sums of q over a group
-    float om[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2];  // sums of p mid
+    // 4 bits: sums of the scaled q over a group, minus what the codes' 1024 + 8 adds to its products, and the scale of
+    // scores (16 bits: the caller's)
+    float qs[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2], qa[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2];
+    float rs[kNt][2];
 
     // The unit's queries as they are in memory: lane (g, c) takes chunks c, c + 4, .. of query head 8 n + g.
     static __device__ __forceinline__ void load_q(uint4 (&x)[kNt][HD / 32], const KvAttnParams& p, const uint8_t* qrow,
@@ -299,35 +303,63 @@ struct KvState {
                               : make_uint4(0, 0, 0, 0);
     }
 
-    __device__ __forceinline__ void begin(const uint4 (&x)[kNt][HD / 32], int lane) {
+    __device__ __forceinline__ void begin(const uint4 (&x)[kNt][HD / 32], int lane, float sl2) {
         const int c = lane & 3;
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
+            if constexpr (kBits == 16) {
 #pragma unroll
-            for (int j = 0; j < HD / 32; ++j) {
-                const uint4 t = x[n][j];
-                if constexpr (kBits == 16) {
-                    q[n][2 * j][0] = t.x; q[n][2 * j][1] = t.y;
-                    q[n][2 * j + 1][0] = t.z; q[n][2 * j + 1][1] = t.w;
-                } else {  // values (i, i + 4) of the chunk beside each other, as the codes of a word
-                    q[n][2 * j][0] = __byte_perm(t.x, t.z, 0x5410);
-                    q[n][2 * j][1] = __byte_perm(t.x, t.z, 0x7632);
-                    q[n][2 * j + 1][0] = __byte_perm(t.y, t.w, 0x5410);
-                    q[n][2 * j + 1][1] = __byte_perm(t.y, t.w, 0x7632);
-                    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-                    float s = 0.f;
+                for (int j = 0; j < HD / 32; ++j) {
+                    q[n][2 * j][0] = x[n][j].x; q[n][2 * j][1] = x[n][j].y;
+                    q[n][2 * j + 1][0] = x[n][j].z; q[n][2 * j + 1][1] = x[n][j].w;
+                }
+                rs[n][0] = rs[n][1] = sl2;
+            } else {
+                // query head g of the tile: its largest |q|, and the power of two that brings it to [1, 2)
+                float f[HD / 32][8], top = 0.f;
+#pragma unroll
+                for (int j = 0; j < HD / 32; ++j) {
+                    const uint32_t w[4] = {x[n][j].x, x[n][j].y, x[n][j].z, x[n][j].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float2 f;
-                        if constexpr (kHalf) f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                        else f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-                        s += f.x + f.y;
+                        float2 v;
+                        if constexpr (kHalf) v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                        else v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+                        f[j][2 * i] = v.x;
+                        f[j][2 * i + 1] = v.y;
+                        top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
                     }
-                    s += __shfl_xor_sync(~0u, s, 1);
-                    s += __shfl_xor_sync(~0u, s, 2);  // query head g's sum, in its four lanes
-                    qs[n][j][0] = __shfl_sync(~0u, s, 8 * c);
-                    qs[n][j][1] = __shfl_sync(~0u, s, 8 * c + 4);
-                    om[n][j][0] = om[n][j][1] = 0.f;
+                }
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                const uint32_t e = __float_as_uint(top) >> 23;  // 255: an infinity (or all NaN): no scaling
+                const float down = e == 255 ? 1.f : __uint_as_float((254u - e) << 23);
+                const float up = e == 255 ? 1.f : __uint_as_float(e << 23);
+                rs[n][0] = sl2 * __shfl_sync(~0u, up, 8 * c);
+                rs[n][1] = sl2 * __shfl_sync(~0u, up, 8 * c + 4);
+#pragma unroll
+                for (int j = 0; j < HD / 32; ++j) {
+                    // values (i, i + 4) of the chunk beside each other, as the codes of a word; the odd ones' codes are
+                    // 16 times theirs
+                    float even = 0.f, odd = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float by = (i & 1) ? down * 0.0625f : down;
+                        const __half2 h = __floats2half2_rn(f[j][i] * by, f[j][i + 4] * by);
+                        q[n][2 * j + (i >> 1)][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
+                        const float2 v = __half22float2(h);
+                        if (i & 1) odd += v.x + v.y;
+                        else even += v.x + v.y;
+                    }
+                    float sum = fmaf(16.f, odd, even), base = -fmaf(1024.f, even + odd, 8.f * sum);
+                    sum += __shfl_xor_sync(~0u, sum, 1);
+                    base += __shfl_xor_sync(~0u, base, 1);
+                    sum += __shfl_xor_sync(~0u, sum, 2);
+                    base += __shfl_xor_sync(~0u, base, 2);
+                    qs[n][j][0] = __shfl_sync(~0u, sum, 8 * c);
+                    qs[n][j][1] = __shfl_sync(~0u, sum, 8 * c + 4);
+                    qa[n][j][0] = __shfl_sync(~0u, base, 8 * c);
+                    qa[n][j][1] = __shfl_sync(~0u, base, 8 * c + 4);
                 }
             }
 #pragma unroll
@@ -365,23 +397,25 @@ struct KvState {
                 float2 scale[2], mid[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) a[i][e] = code_pair<kHalf>(x.k[i][j] >> (4 * e));
+                    const uint32_t w = x.k[i][j], w8 = w >> 8;
+                    a[i][0] = code_pair<false>(w);
+                    a[i][1] = code_pair<true>(w);
+                    a[i][2] = code_pair<false>(w8);
+                    a[i][3] = code_pair<true>(w8);
                     const float2 f = par_of(x.kp[i][j]);
-                    const float m = fmaf(-(kCodeBase<kHalf> + 8.f), f.x, f.y);
                     scale[i] = make_float2(f.x, f.x);
-                    mid[i] = make_float2(m, m);
+                    mid[i] = make_float2(f.y, f.y);
                 }
 #pragma unroll
                 for (int n = 0; n < kNt; ++n) {
                     float t[4];
-                    mma16816_first<kHalf>(t, a[0][0], a[1][0], a[0][1], a[1][1], q[n][2 * j][0], q[n][2 * j][1]);
-                    mma16816<kHalf>(t, a[0][2], a[1][2], a[0][3], a[1][3], q[n][2 * j + 1][0], q[n][2 * j + 1][1]);
-                    const float2 w = make_float2(qs[n][j][0], qs[n][j][1]);
+                    mma16816_first<true>(t, a[0][0], a[1][0], a[0][1], a[1][1], q[n][2 * j][0], q[n][2 * j][1]);
+                    mma16816<true>(t, a[0][2], a[1][2], a[0][3], a[1][3], q[n][2 * j + 1][0], q[n][2 * j + 1][1]);
+                    const float2 w = make_float2(qs[n][j][0], qs[n][j][1]), base = make_float2(qa[n][j][0], qa[n][j][1]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         sum[n][i] = j == 0 ? fmul2(mid[i], w) : ffma2(mid[i], w, sum[n][i]);
-                        sum[n][i] = ffma2(scale[i], make_float2(t[2 * i], t[2 * i + 1]), sum[n][i]);
+                        sum[n][i] = ffma2(scale[i], fadd2(make_float2(t[2 * i], t[2 * i + 1]), base), sum[n][i]);
                     }
                 }
             }
@@ -434,49 +468,51 @@ struct KvState {
                 }
             }
         } else {
+uint32_t b[kNt][2], b2[kNt][2];
 #pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                const float2 par[2] = {par_of(x.vp[0][j]), par_of(x.vp[1][j])};
-                uint32_t b[kNt][2], b2[kNt][2];
+            for (int n = 0; n < kNt; ++n)
 #pragma unroll
-                for (int n = 0; n < kNt; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 sp = make_float2(s[n][2 * i], s[n][2 * i + 1]);
-                        const float2 w = fmul2(sp, make_float2(par[i].x, par[i].x));
-                        const float2 m = ffma2(sp, make_float2(par[i].y, par[i].y), make_float2(om[n][j][0], om[n][j][1]));
-                        om[n][j][0] = m.x;
-                        om[n][j][1] = m.y;
-                        const uint32_t hi = pack_bf16x2(w.x, w.y);
-                        b[n][i] = movmatrix_t(hi);
-                        if constexpr (kSplitP)
-                            b2[n][i] = movmatrix_t(
-                                pack_bf16x2(w.x - __uint_as_float(hi << 16), w.y - __uint_as_float(hi & 0xffff0000u)));
-                    }
-                uint32_t u[2];  // the group's unit of keys 2c, 2c + 1, and of 2c + 8, 2c + 9
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    u[i] = __byte_perm(x.v[2 * i][j / 2], x.v[2 * i + 1][j / 2], (j & 1) ? 0x7632 : 0x5410);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t a0 = code_pair<false>(u[0] >> (8 * t)), a1 = code_pair<false>(u[0] >> (8 * t + 4));
-                    const uint32_t a2 = code_pair<false>(u[1] >> (8 * t)), a3 = code_pair<false>(u[1] >> (8 * t + 4));
-#pragma unroll
-                    for (int n = 0; n < kNt; ++n) {
-                        mma16816<false>(o[n][2 * j + t], a0, a1, a2, a3, b[n][0], b[n][1]);
-                        mma16816<false>(o[n][2 * j + t], kMinus136, kMinus136, kMinus136, kMinus136, b[n][0], b[n][1]);
-                        if constexpr (kSplitP) {
-                            mma16816<false>(o[n][2 * j + t], a0, a1, a2, a3, b2[n][0], b2[n][1]);
-                            mma16816<false>(o[n][2 * j + t], kMinus136, kMinus136, kMinus136, kMinus136, b2[n][0], b2[n][1]);
-                        }
+                for (int i = 0; i < 2; ++i) {
+                    const __half2 hi = __floats2half2_rn(s[n][2 * i], s[n][2 * i + 1]);
+                    b[n][i] = movmatrix_t(*reinterpret_cast<const uint32_t*>(&hi));
+                    if constexpr (kSplitP) {
+                        const float2 f = __half22float2(hi);
+                        b2[n][i] = movmatrix_t(pack_f16x2(s[n][2 * i] - f.x, s[n][2 * i + 1] - f.y));
                     }
                 }
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+                // [i]: keys 2c, 2c + 1, and 2c + 8, 2c + 9, beside each other
+                __half2 v[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t sp = __byte_perm(x.vp[2 * i][j], x.vp[2 * i + 1][j], 0x5410);
+                    const uint32_t mp = __byte_perm(x.vp[2 * i][j], x.vp[2 * i + 1][j], 0x7632);
+                    const __half2 scale = *reinterpret_cast<const __half2*>(&sp), mid = *reinterpret_cast<const __half2*>(&mp);
+                    const uint32_t u = __byte_perm(x.v[2 * i][j / 2], x.v[2 * i + 1][j / 2], (j & 1) ? 0x7632 : 0x5410);
+                    const uint32_t u8 = u >> 8;
+                    v[i][0] = __hfma2(code_value<false>(u), scale, mid);
+                    v[i][1] = __hfma2(code_value<true>(u), scale, mid);
+                    v[i][2] = __hfma2(code_value<false>(u8), scale, mid);
+                    v[i][3] = __hfma2(code_value<true>(u8), scale, mid);
+                }
+                const uint32_t(*a)[4] = reinterpret_cast<const uint32_t(*)[4]>(v);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int n = 0; n < kNt; ++n) {
+                        mma16816<true>(o[n][2 * j + t], a[0][2 * t], a[0][2 * t + 1], a[1][2 * t], a[1][2 * t + 1], b[n][0],
+                                       b[n][1]);
+                        if constexpr (kSplitP)
+                            mma16816<true>(o[n][2 * j + t], a[0][2 * t], a[0][2 * t + 1], a[1][2 * t], a[1][2 * t + 1],
+                                           b2[n][0], b2[n][1]);
+                    }
             }
         }
     }
 
     // One step over a stage; bit i of ok: there is a key i.
-    __device__ __forceinline__ void step(const uint8_t* stage, int g, int c, uint32_t ok, float sl2) {
+    __device__ __forceinline__ void step(const uint8_t* stage, int g, int c, uint32_t ok) {
         constexpr int kSub = KvStage<HD, kBits>::kSub;
         constexpr uint32_t kAll = kSub == 2 ? ~0u : 0xffffu;
         float s[kSub][kNt][4];
@@ -486,7 +522,7 @@ struct KvState {
 #pragma unroll
             for (int n = 0; n < kNt; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[u][n][i] *= sl2;
+                for (int i = 0; i < 4; ++i) s[u][n][i] *= rs[n][i & 1];
         }
         if (ok != kAll) {
 #pragma unroll
@@ -526,9 +562,6 @@ struct KvState {
                         o[n][k][e] *= f;
                         o[n][k][2 + e] *= f;
                     }
-                    if constexpr (kBits == 4)
-#pragma unroll
-                        for (int j = 0; j < kGroups; ++j) om[n][j][e] *= f;
                 }
         }
 #pragma unroll
@@ -709,12 +742,12 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
         issue(stage == 0 ? kStages - 1 : stage - 1, kStages - 1);
         fetch();
         const uint32_t now = note[0];
-        if (now & 1u) st.begin(qn, lane);
+        if (now & 1u) st.begin(qn, lane, p.sl2);
         __syncwarp();
         if (note[1] & 1u) query(qn, note[1]);
         cp_async_wait<kStages - 1>();
         __syncwarp();
-        if (ok[0]) st.step(ring + stage * kStage, g, c, ok[0], p.sl2);
+        if (ok[0]) st.step(ring + stage * kStage, g, c, ok[0]);
         if (now & 2u) {  // join the lanes' and the warps' states
             const int4 d = s_unit[warp][now >> 2];
             const int head = d.y / p.nsub, sub = d.y - head * p.nsub;
@@ -732,20 +765,6 @@ const int join = min(p.gs, 8) * kJoinRow;  // floats of a warp
                     if (g == 0) {
                         s_m[warp][8 * n + 2 * c + e] = st.m[n][e];
                         s_l[warp][8 * n + 2 * c + e] = l;
-                    }
-                    if constexpr (kBits == 4) {
-#pragma unroll
-                        for (int j = 0; j < HD / 32; ++j) {
-                            float t = st.om[n][j][e];
-                            t += __shfl_xor_sync(~0u, t, 4);
-                            t += __shfl_xor_sync(~0u, t, 8);
-                            t += __shfl_xor_sync(~0u, t, 16);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                st.o[n][2 * j + k][e] += t;
-                                st.o[n][2 * j + k][2 + e] += t;
-                            }
-                        }
                     }
                 }
 #pragma unroll

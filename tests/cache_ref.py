@@ -77,8 +77,7 @@ def key_set(p, r, dil, globals_):
 
 
 def attend(q, cache, table, rows, r, dil, globals_, scale):
-    """y [N, Hq, d] float64 (NaN where a row is none), the sums by which its rounding errors are bounded (sum p |v| of
-    the values, or of their scaled codes for 4 bits), and the largest sum of the |terms| of a finite score.  rows: (sequence, position) or None each;
+    """y [N, Hq, d] float64 (NaN where a row is none), the sums p |v| by which its rounding errors are bounded, and the largest sum of the |terms| of a finite score.  rows: (sequence, position) or None each;
     cache: CPU (k, v, k_par, v_par); pages outside the cache hold no keys."""
     k, v, k_par, v_par = cache
     pages, hkv, page = k.shape[:3]
@@ -101,23 +100,25 @@ def attend(q, cache, table, rows, r, dil, globals_, scale):
             b = torch.tensor([w[1] for w in where])
             if k_par is None:
                 kk, vv = k[a, h, b].double(), v[a, h, b].double()
-                part, size = vv, kk.abs()
+                size = kk.abs()
             else:
                 kk, size = values(k[a, h, b], k_par[a, h, b], True)
                 size = size.abs() + (kk - size).abs()
-                vv, part = values(v[a, h, b], v_par[a, h, b], False)
+                vv = values(v[a, h, b], v_par[a, h, b], False)[0]
             size = q[n, heads].double().abs() @ size.T * abs(scale)
             big = max(big, size[torch.isfinite(size)].max().item())
             w = torch.softmax(q[n, heads].double() @ kk.T * scale, -1)
-            y[n, heads], by[n, heads] = w @ vv, w @ part.abs()
+            y[n, heads], by[n, heads] = w @ vv, w @ vv.abs()
     return y, by, big
 
 
 def attend_tolerance(y, by, big, dtype, bits):
-    """Half a step for each rounding: P (times its scale, for 4 bits) to the 16-bit type, and the output; for f16 queries
-    over 4 bits P scale is taken in two bf16 parts.  In fp32: a score is off by at most about 32 steps of 2^-24 of the
-    sum of its |terms| `big` (8 accumulations that may truncate, the group sums, the scaling), which moves P by that share,
-    and so does its base's share the sum; exponentials and sums of P: 2^-12 in all."""
+    """Half a step for each rounding, relative to the sum of p |v|: over 16 bits P as f16 (2^-11) or as two bf16 parts
+    (2^-15); over 4 bits V as f16 (2^-11), and P as f16 with bf16 queries (another 2^-11) or as two f16 parts (2^-20);
+    and the output.  In fp32: a score is off by at most about 32 steps of 2^-24 of the sum of its |terms| `big` (8
+    accumulations that may truncate, the group sums, the scaling), which moves P by that share, and so does its base's
+    share the sum; exponentials and sums of P, and the 1024 times larger sums of 4-bit codes: 2^-12 in all."""
     u = torch.finfo(dtype).eps / 2
-    p = u if bits == 16 or dtype == torch.bfloat16 else 2.0 ** -16
+    half = dtype == torch.float16
+    p = (2.0 ** -11 if half else 2.0 ** -15) if bits == 16 else (2.0 ** -11 + 2.0 ** -20 if half else 2.0 ** -10)
     return p * by + u * y.abs() + (2.0 ** -12 + 2.0 ** -18 * big) * (by + y.abs()) + 1e-7
