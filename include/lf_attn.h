@@ -240,7 +240,8 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  * The cache has n_pages pages of `page` tokens (a power of two, 8..256);
  * table DEVICE int32 [n_seqs, max_pages] names the page that holds positions
  * [i * page, (i + 1) * page) of a sequence, and entries that no token reaches
- * are not read.  A page may be in several tables (a shared prefix) as long as
+ * are not read.  It is read when a call runs, and overlaps nothing a call
+ * writes; nor do rows and cache overlap.  A page may be in several tables (a shared prefix) as long as
  * no call appends to it for two of them.
  *   bits 16: k_cache, v_cache [n_pages, kv_heads, page, d] in `dtype`.
  *   bits 4:  k_cache, v_cache [n_pages, kv_heads, page, d / 2] bytes of codes

@@ -37,9 +37,8 @@
 // rounding (2^-11).  Bound here: instructions (integer ones to spread nibbles,
 // then MMAs), not bytes.
 //
-// Rounding: scores, maxima, sums and O in fp32.  P (at most 2^8, see below)
-// goes to the tensor cores as one f16 (2^-11) with f16 values, and in two bf16
-// parts (2^-15) with bf16 ones: the second part's MMAs are free where the
+// Rounding: scores, maxima, sums and O in fp32.  P goes to the tensor cores as
+// one f16 (2^-11) with f16 values, and in two bf16 parts (2^-15) with bf16 ones: the second part's MMAs are free where the
 // bytes bound it.  With f16 queries over 4 bits, where V is rounded too, P is
 // two f16 parts.
 #pragma once
@@ -282,6 +281,10 @@ template <int HD, int kBits, bool kHalf, int kNt>
 struct KvState {
     static constexpr int kGroups = HD / 32;
     static constexpr bool kSplitP = kBits == 4 && kHalf;
+    // P = 2^(score - base + kLift), at most 2^(kLift + kRoom).  An f16 P is lifted so that a weight 2^-36 of the
+    // largest still counts: a million such keys are 2^-16 of the sum.
+    static constexpr bool kHalfP = kBits == 4 || kHalf;
+    static constexpr float kLift = kHalfP ? 11.f : 0.f, kRoom = kHalfP ? 4.f : 8.f;
     uint32_t q[kNt][HD / 16][2];
     float o[kNt][HD / 16][4];
     float m[kNt][2], l[kNt][2];
@@ -534,7 +537,7 @@ uint32_t b[kNt][2], b2[kNt][2];
                         for (int n = 0; n < kNt; ++n) s[u][n][2 * i] = s[u][n][2 * i + 1] = -INFINITY;
         }
         // The exponent base moves only when a score exceeds it by more than
-        // 2^8 (or it has none yet): sums and O take values up to 2^8 a key.
+        // kRoom (or there is none yet).
         float top[kNt][2];
         bool move = false;
 #pragma unroll
@@ -543,7 +546,7 @@ uint32_t b[kNt][2], b2[kNt][2];
             for (int e = 0; e < 2; ++e) {
                 top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
                 if constexpr (kSub == 2) top[n][e] = fmaxf(top[n][e], fmaxf(s[kSub - 1][n][e], s[kSub - 1][n][2 + e]));
-                move |= top[n][e] > m[n][e] + 8.f;
+                move |= top[n][e] > m[n][e] + kRoom;
             }
         if (__any_sync(~0u, move)) {
 #pragma unroll
@@ -568,7 +571,7 @@ uint32_t b[kNt][2], b2[kNt][2];
         for (int n = 0; n < kNt; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float base = m[n][e] == -INFINITY ? 0.f : m[n][e];  // no score but -inf yet: weights of 0
+                const float base = m[n][e] == -INFINITY ? 0.f : m[n][e] - kLift;  // no score but -inf yet: weights of 0
 #pragma unroll
                 for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -627,8 +630,10 @@ struct KvWalk {
         constexpr int kKeys = block / kKvWarps;
         const int n = b * block + kKeys * warp + (lane & (kKeys - 1));
         if (n >= u.n) return -1;
-        int at = u.first + n * u.step;
-        if (n >= u.n_win) {
+        int at;
+        if (n < u.n_win) {
+            at = u.first + n * u.step;
+        } else {
             at = p.plan.g_list[int64_t(seq) * p.n_global + (n - u.n_win)];
             const int back = pos - at;  // > 0
             if (back % u.step == 0 && back / u.step < u.n_win) return -1;  // in the window

@@ -77,8 +77,8 @@ def key_set(p, r, dil, globals_):
 
 
 def attend(q, cache, table, rows, r, dil, globals_, scale):
-    """y [N, Hq, d] float64 (NaN where a row is none), the sums p |v| by which its rounding errors are bounded, and the largest sum of the |terms| of a finite score.  rows: (sequence, position) or None each;
-    cache: CPU (k, v, k_par, v_par); pages outside the cache hold no keys."""
+    """y [N, Hq, d] float64 (NaN where a row is none), the sums p |v| by which its rounding errors are bounded, and the
+    largest sum of the |terms| of a finite score.  rows: (sequence, position) or None each; cache: CPU (k, v, k_par, v_par); pages outside the cache hold no keys."""
     k, v, k_par, v_par = cache
     pages, hkv, page = k.shape[:3]
     N, hq, d = q.shape

@@ -272,6 +272,27 @@ def test_scores_far_apart():
     s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
 
 
+@pytest.mark.parametrize("dtype,bits", [(F16, 16), (BF16, 16), (F16, 4), (BF16, 4)])
+def test_a_long_tail_of_small_weights_counts(dtype, bits):
+    """One key at score 0 with value 0, and 200000 at about 2^-25.5 of its weight, each under f16's smallest half step,
+    with values of 100: their sum is not small."""
+    T = 200000
+    s = Step(28, dtype, 16, [1], [T - 1], 1, 1, 64, 256, FULL, pages_more=0)
+    k, v = torch.zeros(T, 1, 64), torch.zeros(T, 1, 64)
+    k[1:, 0, 0], v[1:] = -8.0, 100.0
+    s.q.zero_()
+    s.q[0, 0, 0] = 17.7
+    cu, old = torch.tensor([0, T], dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda()
+    s.bits, s.cache = bits, kv_cache.KVCache.empty(s.cpu[0].shape[0], 1, 256, 64, dtype, bits)
+    fill = kv_cache.Plan(s.cache, s.table.cuda(), cu, old, T, 1)
+    kv_cache.append(s.cache, fill, k.to(dtype).cuda(), v.to(dtype).cuda())
+    s.plan = kv_cache.Plan(s.cache, s.table.cuda(), s.cu.cuda(), s.context.cuda(), 1, 1)
+    s.cpu = [None if t is None else t.cpu() for t in (s.cache.k, s.cache.v, s.cache.k_par, s.cache.v_par)]
+    got = kv_cache.fwd(s.cache, s.plan, s.q.cuda(), scale=0.125)
+    assert 0.2 < got.min() < 1
+    s.check(got, scale=0.125)
+
+
 def test_strides_and_rows_that_are_none():
     s = Step(13, BF16, 16, [2, 1], [40, 9], 6, 2, 64, 16, 20, spare_rows=4).to_gpu()
     packed = torch.randn(s.N, 10, 64, generator=gen(1)).to(BF16)
