@@ -102,12 +102,12 @@ class Plan:
         self.workspace_bytes = lf_attn.load().lf_attn_cache_workspace_bytes(
             self.n_tokens, self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.d, self.bits,
             self.r)
-        self.buffer = _on_stream(stream, self._inputs(),
+        self.buffer = _on_stream(stream, context.get_device(), self._inputs(),
                                  lambda raw: torch.empty(size, dtype=torch.uint8, device=context.device))
         self.refresh(stream)
 
     def _inputs(self):
-        return [t for t in (self.cu_tokens, self.context, self.table, self.global_idx) if t is not None]
+        return self.cu_tokens, self.context, self.table, self.global_idx
 
     def refresh(self, stream: Optional[torch.cuda.Stream] = None) -> "Plan":
         """Lays the step out again, from what cu_tokens, context and global_idx hold when the call runs."""
@@ -120,7 +120,7 @@ class Plan:
             if st != 0:
                 raise LfAttnError(st, "lf_attn_cache_plan")
 
-        _on_stream(stream, self._inputs() + [self.buffer], call)
+        _on_stream(stream, self.context.get_device(), (*self._inputs(), self.buffer), call)
         return self
 
     def _check(self, cache: KVCache):
@@ -179,8 +179,7 @@ def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Opti
         for t in held:
             _rows(t, n, hkv, d, dtype, "held")
     rot = _check_freqs(freqs, d)
-    used = [t for t in (k, v, plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par, q, freqs, q_out, hk,
-                        hv) if t is not None]
+    used = (k, v, plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par, q, freqs, q_out, hk, hv)
 
     def call(raw):
         nonlocal q_out, hk, hv
@@ -201,7 +200,7 @@ def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Opti
                 raise LfAttnError(st, "lf_attn_cache_append")
         return (q_out, hk, hv) if hk is not None else q_out
 
-    return _on_stream(stream, used, call)
+    return _on_stream(stream, k.get_device(), used, call)
 
 
 def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = None,
@@ -214,8 +213,7 @@ def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = No
     n, heads, d, dtype = plan.n_tokens, plan.q_heads, cache.d, q.dtype
     code = _code(cache, dtype)
     qs = _rows(q, n, heads, d, dtype, "q")
-    used = [t for t in (q, plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par, out, workspace)
-            if t is not None]
+    used = (q, plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par, out, workspace)
     if out is not None:
         _rows(out, n, heads, d, dtype, "out")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
@@ -237,4 +235,4 @@ def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = No
             raise LfAttnError(st, "lf_attn_cache_fwd")
         return y
 
-    return _on_stream(stream, used, call)
+    return _on_stream(stream, q.get_device(), used, call)

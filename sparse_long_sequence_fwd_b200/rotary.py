@@ -59,15 +59,14 @@ _CODES = {torch.float32: lf_attn.LF_F32, torch.bfloat16: lf_attn.LF_BF16, torch.
 _NONE = (0, 0, 0)
 
 
-def _on_stream(stream: Optional[torch.cuda.Stream], tensors, call):
-    """call(raw stream) with ``stream`` (default: the device's current one) as the current stream of the tensors'
-    device: what the call allocates belongs to that stream, and tensors are marked as used by a stream that is not
-    the current one."""
-    index = tensors[0].get_device()
+def _on_stream(stream: Optional[torch.cuda.Stream], index: int, tensors, call):
+    """call(raw stream) with ``stream`` (default: the device's current one) as the current stream of device ``index``,
+    which all of ``tensors`` (None: absent) must be on: what the call allocates belongs to that stream, and tensors are
+    marked as used by a stream that is not the current one."""
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
     for t in tensors:
-        if t.get_device() != index:
+        if t is not None and t.get_device() != index:
             raise ValueError("all tensors must be on one device")
     if stream is None:
         if torch._C._cuda_getDevice() == index:
@@ -79,7 +78,8 @@ def _on_stream(stream: Optional[torch.cuda.Stream], tensors, call):
     with torch.cuda.device(index):
         if stream != torch.cuda.current_stream() and not torch.cuda.is_current_stream_capturing():
             for t in tensors:
-                t.record_stream(stream)
+                if t is not None:
+                    t.record_stream(stream)
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
 
@@ -106,11 +106,12 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
     in_code = _CODES.get(dtype)
     if in_code is None:
         raise TypeError("q, k, v must be float32, bfloat16 or float16, got %s" % dtype)
-    rows, heads, strides, used = (q, k, v), [], [], []
+    rows, heads, strides, at = (q, k, v), [], [], []
     for t in rows:
         if t is None:
             heads.append(0)
             strides += _NONE
+            at.append(None)
             continue
         shape, stride = t.shape, t.stride()
         if len(shape) != 4:
@@ -123,7 +124,7 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
             raise ValueError("the d values of a row must be contiguous")
         heads.append(shape[1])
         strides += stride[:3]
-        used.append(t)
+        at.append(t.data_ptr())
     if heads[1] != heads[2] and k is not None and v is not None:
         raise ValueError("k and v must have the same heads")
     rot = _check_freqs(f, d)
@@ -135,11 +136,9 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
         if len(shape) == 2:
             pos_stride = pos.stride(0)
         pos_at = pos.data_ptr()
-        used.append(pos)
-    if f is not None:
-        used.append(f)
     if out is None:
         out_dtype = out_dtype or dtype
+        used = (q, k, v, f, pos)
     else:
         out = tuple(out)
         if len(out) != 3:
@@ -153,7 +152,7 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
                     raise TypeError("out must share one dtype")
                 if d > 1 and o.stride(3) != 1:
                     raise ValueError("the d values of a row must be contiguous")
-                used.append(o)
+        used = (q, k, v, f, pos, *out)
     out_code = _CODES.get(out_dtype)
     if out_code is None:
         raise TypeError("out must be float32, bfloat16 or float16, got %s" % out_dtype)
@@ -161,9 +160,12 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
     def call(raw):
         y = out
         if y is None:
-            kw = {} if out_dtype is dtype else {"dtype": out_dtype}
-            y = tuple([None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format, **kw)
-                       for t in rows])
+            if out_dtype is dtype:
+                y = tuple([None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
+                           for t in rows])
+            else:
+                y = tuple([None if t is None else
+                           torch.empty_like(t, dtype=out_dtype, memory_format=torch.contiguous_format) for t in rows])
             n = T * d
             strides.extend((heads[0] * n, n, d, heads[1] * n, n, d, heads[2] * n, n, d))
         else:
@@ -171,15 +173,16 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
                 strides.extend(_NONE if t is None else t.stride()[:3])
         if B == 0 or T == 0 or not any(heads):  # nothing to turn: empty tensors have no address
             return y
+        for t in y:
+            at.append(None if t is None else t.data_ptr())
         st = lf_attn.load().lf_attn_rotary(
-            *[None if t is None else t.data_ptr() for t in rows + y], _PACK18(*strides), B, heads[0],
-            heads[1] or heads[2], T, d, pos_at, pos_stride, f.data_ptr() if rot else None, rot,
-            1 if interleaved else 0, inverse, amplitude, in_code, out_code, raw)
+            *at, _PACK18(*strides), B, heads[0], heads[1] or heads[2], T, d, pos_at, pos_stride,
+            f.data_ptr() if rot else None, rot, 1 if interleaved else 0, inverse, amplitude, in_code, out_code, raw)
         if st != 0:
             raise LfAttnError(st, "lf_attn_rotary")
         return y
 
-    return _on_stream(stream, used, call)
+    return _on_stream(stream, first.get_device(), used, call)
 
 
 def fwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, *,
