@@ -354,7 +354,8 @@ lf_status lf_attn_device_status(void* stream, uint32_t* flags);
 /* Text for a status code (static storage). */
 const char* lf_attn_strerror(lf_status status);
 
-/* Frees the workspaces of every device this process used. */
+/* Frees the workspaces and status words of every device this process used
+ * (graphs captured before hold them: they are not replayed after). */
 void lf_attn_release(void);
 
 /* Bytes of device workspace lf_attn_fwd needs for these sizes. */

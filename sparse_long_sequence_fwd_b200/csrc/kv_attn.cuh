@@ -7,10 +7,9 @@
 // zeros), whatever the cache holds there.
 //
 // Bound: the cache's bytes.  A key's row is read once for at most 16 query
-// heads, so the intensity is at most 16 flops a byte in 16 bits.  The rows
-// go from global memory straight to registers in the layout that the
-// warp-level MMA takes, with no staging in shared memory: both products are
-// written transposed, S^T = K Q^T and O^T = V^T P^T (m16n8k16 with 16 keys,
+// heads, so the intensity is at most 16 flops a byte in 16 bits (measured: 16
+// sequences of 16384 to 32768 tokens, 8 kv heads of 128, bf16: 1.63 GB in 244
+// us, the rate of a plain copy).  Both products are written transposed, S^T = K Q^T and O^T = V^T P^T (m16n8k16 with 16 keys,
 // or 16 value dimensions, as M and 8 query heads as N), which needs half the
 // MMAs and accumulators of the other order when there are few heads.
 //   lane (g, c) = (lane / 4, lane % 4).  K: the lane reads the 16-byte chunks
@@ -22,8 +21,8 @@
 // A CTA's four warps take 16 or 32 keys each of a 64- or 128-key block; a warp
 // keeps its own running maximum, sum and O, joined through shared memory when
 // the unit's piece ends.  Each warp has a ring of stages in shared memory that
-// it fills itself with cp.async, two blocks ahead of the one it computes,
-// across unit boundaries too (short windows are a few blocks long); the page
+// it fills itself with cp.async, one block ahead of the one it computes (two
+// ahead measured 4 % slower over long sequences), across unit boundaries too (short windows are a few blocks long); the page
 // table is read one block before that, and the next unit's queries while the
 // last block of a unit is computed.
 //
@@ -34,13 +33,15 @@
 // fp32 sum (what that loses is 1024 steps of 2^-24 of the q sum).  Queries are
 // brought to [-2, 2] by a power of two for it, which f16 holds exactly down to
 // 2^-14 of the largest, and to 2^-25 of it below.  V is made f16 values, one
-// rounding (2^-11).  Bound here: instructions (integer ones to spread nibbles,
-// then MMAs), not bytes.
+// rounding (2^-11).  Bound here: instructions, about 28 a key and warp at d =
+// 128, half of them integer ones to spread nibbles (4 sequences of 32768 to
+// 65536 tokens, 8 kv heads of 128: 264 MB in 82 us, 49 % of the copy rate; 51
+// us with the products left out).
 //
 // Rounding: scores, maxima, sums and O in fp32.  P goes to the tensor cores as
-// one f16 (2^-11) with f16 values, and in two bf16 parts (2^-15) with bf16 ones: the second part's MMAs are free where the
-// bytes bound it.  With f16 queries over 4 bits, where V is rounded too, P is
-// two f16 parts.
+// one f16 (2^-11) with f16 values, and in two bf16 parts (2^-15) with bf16
+// ones: the second part's MMAs are free where the bytes bound it.  With f16
+// queries over 4 bits, where V is rounded too, P is two f16 parts.
 #pragma once
 #include "kv_plan.cuh"
 #include "lf_common.cuh"
@@ -54,14 +55,14 @@ constexpr int kStages = 2;
 
 // Steps of 16 keys that a warp takes at once: two over 4 bits, so that what a
 // step costs besides its keys (the walk, the vote on the base) is paid half as
-// often (instructions bound it: 102 -> 88 us at 1.6 M keys of 2 x 80 bytes);
-// one over 16 bits, where 32 rows a stage would leave an SM half the warps
-// (d = 64, batch of short windows: 7.4 against 9.1 us).
+// often (102 -> 88 us at 1.6 M keys of d = 128); one over 16 bits, where 32
+// rows a stage would leave an SM half the warps (d = 64, batch of short
+// windows: 7.4 against 9.1 us).
 __host__ __device__ constexpr int kv_sub(int bits) { return bits == 16 ? 1 : 2; }
 __host__ __device__ constexpr int kv_block(int bits) { return kKvWarps * 16 * kv_sub(bits); }
 
-// CTAs of four warps that an SM holds at once: by the ring's shared memory
-// (16 bits: 48 KB a CTA at d = 64, 96 KB at 128), else by registers.
+// CTAs of four warps that an SM holds at once, by registers (128 to 255 a
+// thread).
 __host__ __device__ constexpr int kv_ctas_per_sm(int d, int bits, bool two) {
     return d == 64 ? (two || bits == 4 ? 3 : 4) : (bits == 16 || two ? 2 : 3);
 }
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int s = blockIdx.x;
     grid_dep_launch();
-    const KvStart start = p.plan.start[s];
+    const KvStart start = p.plan.start[s];  // (at a fixed place of any plan)
     if (p.plan.sig[1] != p.sig) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadPlan);
         return;
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
             const int4 d = s_unit[warp][now >> 2];
             const int head = d.y / p.nsub, sub = d.y - head * p.nsub;
             const int heads = min(p.gs, p.group - sub * p.gs), qh = head * p.group + sub * p.gs;
-const int join = min(p.gs, 8) * kJoinRow;  // floats of a warp
+            const int join = min(p.gs, 8) * kJoinRow;  // floats of a warp
             float* part = p.part + int64_t(d.w) * p.gs * kv_piece_row(HD);
 #pragma unroll
             for (int n = 0; n < kNt; ++n) {

@@ -68,17 +68,18 @@ struct KvShape {  // what a plan is made for
     int32_t dil[kMaxHeads];
 };
 
-// Places in the plan buffer (bytes, 256-byte aligned).
+// Places in the plan buffer (bytes, 256-byte aligned).  What the attention
+// reads before it has seen that the plan is its own lies at fixed places.
 struct KvPlanLayout {
-    size_t prefix, start, cut, seq, pos, ng, gcount, glist, total;
+    size_t start, cut, prefix, seq, pos, ng, gcount, glist, total;
 };
 inline KvPlanLayout kv_plan_layout(int S, int N, int n_global) {
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     KvPlanLayout L;
-    L.prefix = 256;
-    L.start = up(L.prefix + sizeof(int64_t) * size_t(N));
+    L.start = 256;
     L.cut = up(L.start + sizeof(KvStart) * kKvMaxCtas);
-    L.seq = up(L.cut + sizeof(KvCut) * kKvMaxCtas);
+    L.prefix = up(L.cut + sizeof(KvCut) * kKvMaxCtas);
+    L.seq = up(L.prefix + sizeof(int64_t) * size_t(N));
     L.pos = up(L.seq + sizeof(int32_t) * size_t(N));
     L.ng = up(L.pos + sizeof(int32_t) * size_t(N));
     L.gcount = up(L.ng + sizeof(int32_t) * size_t(N));

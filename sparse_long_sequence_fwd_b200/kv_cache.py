@@ -76,7 +76,9 @@ class Plan:
     """One step over caches shaped as ``cache``: rows [cu_tokens[s], cu_tokens[s+1]) of the step's n_tokens rows are
     sequence s's new tokens, at positions context[s] on; rows behind the last sequence are no tokens.  ``table``:
     int32 [n_seqs, max_pages]; ``global_idx``: int32 [n_seqs, n_global], any order; ``dil``: an int or one per kv head;
-    ``r``: how many (dilated) positions back a token sees beside the global ones, None for all of them."""
+    ``r``: how many (dilated) positions back a token sees beside the global ones, None for all of them.
+
+    ``table`` is read when append and fwd run, the other tensors when the plan is made or refreshed."""
 
     def __init__(self, cache: KVCache, table: torch.Tensor, cu_tokens: torch.Tensor, context: torch.Tensor,
                  n_tokens: int, q_heads: int, r: Optional[int] = None, dil=None,
@@ -195,7 +197,8 @@ def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Opti
                 k.data_ptr(), v.data_ptr(), _at(q), _at(hk), _at(hv), _at(q_out), _PACK12(*strides), cache.k.data_ptr(),
                 cache.v.data_ptr(), _at(cache.k_par), _at(cache.v_par), cache.pages, cache.page, plan.table.data_ptr(),
                 plan.max_pages, plan.buffer.data_ptr(), plan.n_seqs, n, plan.n_global, plan.q_heads, hkv, d,
-                freqs.data_ptr() if rot else None, rot, 1 if interleaved else 0, amplitude, code, cache.bits, raw)
+                freqs.data_ptr() if rot else None, rot, 1 if interleaved else 0, float(amplitude), code, cache.bits,
+                raw)
             if st != 0:
                 raise LfAttnError(st, "lf_attn_cache_append")
         return (q_out, hk, hv) if hk is not None else q_out
@@ -230,7 +233,7 @@ def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = No
             q.data_ptr(), y.data_ptr(), _PACK4(*qs, *y.stride()[:2]), cache.k.data_ptr(), cache.v.data_ptr(),
             _at(cache.k_par), _at(cache.v_par), cache.pages, cache.page, plan.table.data_ptr(), plan.max_pages,
             plan.buffer.data_ptr(), plan.n_seqs, n, plan.n_global, heads, cache.kv_heads, d, plan.r, plan.dil,
-            d ** -0.5 if scale is None else scale, code, cache.bits, _at(ws), 0 if ws is None else ws.numel(), raw)
+            d ** -0.5 if scale is None else float(scale), code, cache.bits, _at(ws), 0 if ws is None else ws.numel(), raw)
         if st != 0:
             raise LfAttnError(st, "lf_attn_cache_fwd")
         return y

@@ -177,7 +177,7 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
             at.append(None if t is None else t.data_ptr())
         st = lf_attn.load().lf_attn_rotary(
             *at, _PACK18(*strides), B, heads[0], heads[1] or heads[2], T, d, pos_at, pos_stride,
-            f.data_ptr() if rot else None, rot, 1 if interleaved else 0, inverse, amplitude, in_code, out_code, raw)
+            f.data_ptr() if rot else None, rot, 1 if interleaved else 0, inverse, float(amplitude), in_code, out_code, raw)
         if st != 0:
             raise LfAttnError(st, "lf_attn_rotary")
         return y

@@ -50,6 +50,7 @@ ROTARY_ORDER = ("q k v qo ko vo s B hq hkv T d pos ps f rot inter inv amp ti to 
     (dict(s=i64(*[-8192, 4096, 64] * 6)), INVALID), (dict(s=i64(*[1 << 60, 4096, 64] * 6)), INVALID),
     (dict(ti=1, to=0), UNSUPPORTED), (dict(ti=1, to=2), UNSUPPORTED), (dict(d=258), UNSUPPORTED),
     (dict(B=65536, s=i64(*[1, 1, 1] * 6), q=FAKE, qo=1 << 30, k=None, ko=None, v=None, vo=None), UNSUPPORTED),
+    (dict(s=i64(*[0, 1 << 31, 64] + [8192, 4096, 64] * 5), T=2), UNSUPPORTED),
     (dict(B=0), OK), (dict(T=0), OK), (dict(hq=0, hkv=0), OK),
 ])
 def test_rotary_refusals(lib, kw, code):
@@ -103,7 +104,7 @@ APPEND_ORDER = "k v q hk hv qo s kc vc kp vp pages page table mp plan S N ng hq 
     (dict(pages=0), INVALID), (dict(k=FAKE + 1), INVALID), (dict(qo=3 * FAKE + 64), INVALID), (dict(hk=FAKE), INVALID),
     (dict(s=i64(*[256, 64] * 5 + [256, 0])), INVALID), (dict(t=5), INVALID),
     (dict(t=0), UNSUPPORTED), (dict(d=32, rot=32), UNSUPPORTED), (dict(pages=1 << 27), UNSUPPORTED),
-    (dict(page=24), UNSUPPORTED), (dict(N=0), OK),
+    (dict(page=24), UNSUPPORTED), (dict(s=i64(*[1 << 31, 64] + [256, 64] * 5), k=1 << 40), UNSUPPORTED), (dict(N=0), OK),
 ])
 def test_append_refusals(lib, kw, code):
     assert call(lib.lf_attn_cache_append, APPEND, APPEND_ORDER, **kw) == code

@@ -53,6 +53,10 @@ ROTARY = [  # B, T, hq, hkv, d, rot, interleaved, in, out
     (1, 9, 2, 2, 256, 256, False, F16, F16),
     (1, 33, 2, 2, 6, 2, False, F32, F32),
     (2, 20, 4, 4, 64, 0, False, BF16, BF16),       # a copy into another layout
+    (1, 700, 3, 1, 80, 80, True, BF16, BF16),      # five items a row
+    (2, 311, 1, 1, 48, 16, False, F16, F16),
+    (1, 5, 128, 128, 128, 128, False, BF16, BF16),
+    (1, 3001, 1, 2, 64, 40, True, BF16, BF16),
 ]
 
 
@@ -189,6 +193,8 @@ ATTEND = {  # dtype, bits, new, old, hq, hkv, d, page, r, dil, globals
     "shared_12": (F16, 16, [1], [257], 12, 1, 64, 64, 100, 1, [[0, 1]]),
     "shared_16_d128": (BF16, 16, [1], [300], 32, 2, 128, 16, FULL, 1, None),
     "shared_40": (BF16, 16, [2], [300], 40, 1, 64, 16, 64, 1, [[2]]),
+    "shared_17": (BF16, 16, [1, 1], [90, 200], 34, 2, 64, 32, 64, 1, [[5, 80]] * 2),
+    "shared_20_f16_4": (F16, 4, [1], [300], 20, 1, 64, 32, FULL, 1, None),
     "shared_128": (F16, 16, [1], [65], 128, 1, 128, 256, FULL, 1, None),
     "drafts": (BF16, 16, [5, 0, 3, 1], [100, 10, 0, 63], 4, 2, 64, 32, 16, 1, [[0, 102], [0, 1], [1, 1], [0, 2]]),
     "prompt": (BF16, 16, [150], [0], 2, 1, 64, 64, 32, 1, [[0]]),
@@ -215,6 +221,15 @@ def test_attention_over_the_cache(name):
 @pytest.mark.parametrize("bits", [16, 4])
 def test_long_ragged_batch(bits):
     s = Step(60 + bits, BF16, bits, [1] * 6, [5000, 1, 2047, 64, 63, 900], 6, 3, 64, 64, FULL).to_gpu()
+    s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
+
+
+def test_more_sequences_and_rows_than_fit_shared_memory():
+    """The plan's searches in global memory: 4500 sequences, some without new tokens, and 1500 rows of one."""
+    new = [0 if i % 7 == 3 else 1 for i in range(4500)]
+    s = Step(70, BF16, 16, new, [i % 13 for i in range(4500)], 2, 1, 64, 8, 6, globals_=[[0, 2]] * 4500).to_gpu()
+    s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
+    s = Step(71, F16, 16, [1500, 3], [40, 0], 1, 1, 64, 64, 20, dil=3).to_gpu()
     s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
 
 
@@ -422,6 +437,20 @@ def test_append(case):
             assert torch.equal(b.view(torch.uint8), a.view(torch.uint8))
 
 
+def test_append_into_given_rows_and_without_queries():
+    s = Step(19, F16, 4, [6, 2], [250, 9], 4, 2, 64, 256, 4, spare_rows=1).to_gpu()
+    wide = torch.full((s.N, 2, 2, 72), 9.0, dtype=F16, device="cuda")
+    hk, hv = wide[:, 0, :, 4:68], wide[:, 1, :, 4:68]       # rows off the 16-byte grid
+    none, a, b = kv_cache.append(s.cache, s.plan, s.k.cuda(), s.v.cuda(), held=(hk, hv))
+    assert none is None and a is hk and b is hv
+    for x, h in ((s.k, hk), (s.v, hv)):
+        codes, par = ref.quantise(x[:8])
+        par = par.double()
+        want = (par[..., 1:] + par[..., :1] * (codes.double() - 8).unflatten(-1, (2, 32))).flatten(-2)
+        assert torch.equal(h[:8].cpu(), want.to(F16))
+    assert (wide[8] == 9).all() and (wide[..., :4] == 9).all() and (wide[..., 68:] == 9).all()
+
+
 def test_append_quantises_by_the_formula():
     """Untouched keys (no turn): constant groups, single outliers, ties, tiny and large values, infinities and NaN."""
     s = Step(18, BF16, 4, [12], [3], 2, 2, 64, 16, 4)
@@ -435,13 +464,15 @@ def test_append_quantises_by_the_formula():
     k[6] *= 1e4
     k[7] = -k[7].abs()
     k[8, 0, 3], k[8, 1, 40], k[9, 0, 33] = math.nan, math.inf, -math.inf
+    k[10, 0, 3], k[10, 1, 60] = 65536.0, -1e30       # past fp16
+    k[11] = 60000 + k[11]
     s.k = k.to(BF16)
     s.to_gpu()
     _, hk, _ = kv_cache.append(s.cache, s.plan, s.k.cuda(), s.v.cuda(), held=True)
     pos = torch.tensor([p for _, p in s.rows])
     page = s.table[0].long()[pos // 16]
     codes, par = ref.quantise(s.k)
-    broken = ~torch.isfinite(s.k.float()).unflatten(-1, (2, 32)).all(-1)
+    broken = ~(s.k.float().abs() <= 65504).unflatten(-1, (2, 32)).all(-1)
     got_par, got = s.cache.k_par.cpu()[page, :, pos % 16], ref.unpack(s.cache.k.cpu()[page, :, pos % 16], True)
     assert torch.isnan(got_par[..., 1][broken]).all() and torch.isnan(hk.cpu().unflatten(-1, (2, 32))[broken]).all()
     assert torch.equal(got_par[~broken], par[~broken])
@@ -558,6 +589,19 @@ def test_streams_and_overlapping_calls():
         a.check(x)
         b.check(y)
         assert torch.equal(x, ys[0][0]) and torch.equal(y, ys[0][1])
+
+
+def test_rotary_on_another_stream_than_the_current_one():
+    q = torch.randn(2, 3, 5000, 64, generator=gen(6)).cuda()
+    f, side = rotary.freqs(64, device="cuda"), torch.cuda.Stream()
+    want = rotary.fwd(q, freqs=f)[0]
+    x = q.clone()
+    torch.cuda.synchronize()
+    got = rotary.fwd(x, freqs=f, stream=side)[0]
+    del x
+    torch.full_like(q, 7.0)  # takes memory of x only once the other stream is done with it
+    side.synchronize()
+    assert torch.equal(got, want)
 
 
 def test_captured_step_follows_its_inputs():
