@@ -336,7 +336,7 @@ struct KvState {
                 }
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                const uint32_t e = __float_as_uint(top) >> 23;  // 255: an infinity (or all NaN): no scaling
+                const uint32_t x8 = __float_as_uint(top) >> 23, e = x8 == 254 ? 253 : x8;  // 255: an infinity: no scaling
                 const float down = e == 255 ? 1.f : __uint_as_float((254u - e) << 23);
                 const float up = e == 255 ? 1.f : __uint_as_float(e << 23);
                 rs[n][0] = sl2 * __shfl_sync(~0u, up, 8 * c);
