@@ -824,8 +824,12 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
 }
 
 // Joins the pieces of the unit that CTA s of the attention began and CTA
-// cut.last ended, in CTA order.  grid: (G, query heads of a unit), HD
-// threads, one per dimension; the attention's programmatic dependent.
+// cut.last ended: y = sum of 2^(m_k - M) O_k over sum of 2^(m_k - M) l_k, M =
+// max m_k, in CTA order.  grid: (G, query heads of a unit), HD threads, one
+// per dimension; the attention's programmatic dependent.  Bound: latency (all
+// pieces' m and l at once, then their O eight at a time: 6 us with its launch;
+// one piece after the other took 49 us at 12 pieces of 8 heads).  A grid of
+// cut units alone, listed by the plan, measured 0.9 us slower.
 template <int HD, bool kHalf>
 __global__ void __launch_bounds__(HD) kv_merge_kernel(const __grid_constant__ KvAttnParams p) {
     __shared__ float s_w[HD], s_red[2];

@@ -19,7 +19,8 @@
 // the units that begin in its range, and nothing is merged.  (A global row,
 // which sees every key, is then one CTA's work too.)
 //
-// Bound: latency (a few KB).  The global lists take one CTA per sequence; the
+// Bound: latency (a few KB; 6 to 16 us for 1 to 64 sequences, 32 us for a
+// prompt of 16384 rows, once for all layers of a step).  The global lists take one CTA per sequence; the
 // rows, their prefix sum and the split one CTA in all, since each needs the
 // whole of the one before, with what is searched held in shared memory.
 #pragma once
