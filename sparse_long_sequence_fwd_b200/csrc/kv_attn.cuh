@@ -38,10 +38,10 @@
 // 65536 tokens, 8 kv heads of 128: 264 MB in 82 us, 49 % of the copy rate; 51
 // us with the products left out).
 //
-// Rounding: scores, maxima, sums and O in fp32.  P goes to the tensor cores as
-// one f16 (2^-11) with f16 values, and in two bf16 parts (2^-15) with bf16
-// ones: the second part's MMAs are free where the bytes bound it.  With f16
-// queries over 4 bits, where V is rounded too, P is two f16 parts.
+// Rounding: scores, maxima, sums and O in fp32.  P goes to the tensor cores in
+// two bf16 (2^-15) or f16 parts (2^-20): the second part's MMAs are free where
+// the bytes bound it.  Over 4 bits, where V is rounded to f16 anyway, P is one
+// f16 (2^-11) with bf16 queries and two with f16 ones.
 #pragma once
 #include "kv_plan.cuh"
 #include "lf_common.cuh"
@@ -126,6 +126,12 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint3
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2_rz(float lo, float hi) {  // toward 0
+    uint32_t y;
+    asm("cvt.rz.f16x2.f32 %0, %2, %1;" : "=r"(y) : "f"(lo), "f"(hi));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
@@ -443,14 +449,18 @@ struct KvState {
             for (int n = 0; n < kNt; ++n) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
+                    // toward 0, and what that leaves: never 0 or less, so that it times an infinite value is one
+                    const float p0 = s[n][2 * i], p1 = s[n][2 * i + 1];
                     if constexpr (kHalf) {
-                        b[n][i] = movmatrix_t(pack_f16x2(s[n][2 * i], s[n][2 * i + 1]));
-                    } else {  // the upper halves, and what they leave: never 0 or less, so that it times an infinite value is one
-                        const uint32_t u = __float_as_uint(s[n][2 * i]), w = __float_as_uint(s[n][2 * i + 1]);
+                        const uint32_t hi = pack_f16x2_rz(p0, p1);
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                        b[n][i] = movmatrix_t(hi);
+                        b2[n][i] = movmatrix_t(pack_f16x2(fmaxf(p0 - f.x, 0x1p-24f), fmaxf(p1 - f.y, 0x1p-24f)));
+                    } else {
+                        const uint32_t u = __float_as_uint(p0), w = __float_as_uint(p1);
                         b[n][i] = movmatrix_t(__byte_perm(u, w, 0x7632));
-                        b2[n][i] = movmatrix_t(
-                            pack_bf16x2(fmaxf(s[n][2 * i] - __uint_as_float(u & 0xffff0000u), 1e-37f),
-                                        fmaxf(s[n][2 * i + 1] - __uint_as_float(w & 0xffff0000u), 1e-37f)));
+                        b2[n][i] = movmatrix_t(pack_bf16x2(fmaxf(p0 - __uint_as_float(u & 0xffff0000u), 1e-37f),
+                                                           fmaxf(p1 - __uint_as_float(w & 0xffff0000u), 1e-37f)));
                     }
                 }
             }
@@ -467,7 +477,7 @@ struct KvState {
 #pragma unroll
                     for (int n = 0; n < kNt; ++n) {
                         mma16816<kHalf>(o[n][4 * j + t], a0, a1, a2, a3, b[n][0], b[n][1]);
-                        if constexpr (!kHalf) mma16816<kHalf>(o[n][4 * j + t], a0, a1, a2, a3, b2[n][0], b2[n][1]);
+                        mma16816<kHalf>(o[n][4 * j + t], a0, a1, a2, a3, b2[n][0], b2[n][1]);
                     }
                 }
             }

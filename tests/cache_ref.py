@@ -113,12 +113,12 @@ def attend(q, cache, table, rows, r, dil, globals_, scale):
 
 
 def attend_tolerance(y, by, big, dtype, bits):
-    """Half a step for each rounding, relative to the sum of p |v|: over 16 bits P as f16 (2^-11) or as two bf16 parts
-    (2^-15); over 4 bits V as f16 (2^-11), and P as f16 with bf16 queries (another 2^-11) or as two f16 parts (2^-20);
+    """Half a step for each rounding, relative to the sum of p |v|: over 16 bits P as two bf16 parts (2^-15) or two
+    f16 ones (2^-20); over 4 bits V as f16 (2^-11), and P as f16 with bf16 queries (another 2^-11) or as two f16 parts (2^-20);
     and the output.  In fp32: a score is off by at most about 32 steps of 2^-24 of the sum of its |terms| `big` (8
     accumulations that may truncate, the group sums, the scaling), which moves P by that share, and so does its base's
     share the sum; exponentials and sums of P, and the 1024 times larger sums of 4-bit codes: 2^-12 in all."""
     u = torch.finfo(dtype).eps / 2
     half = dtype == torch.float16
-    p = (2.0 ** -11 if half else 2.0 ** -15) if bits == 16 else (2.0 ** -11 + 2.0 ** -20 if half else 2.0 ** -10)
+    p = (2.0 ** -20 if half else 2.0 ** -15) if bits == 16 else (2.0 ** -11 + 2.0 ** -20 if half else 2.0 ** -10)
     return p * by + u * y.abs() + (2.0 ** -12 + 2.0 ** -18 * big) * (by + y.abs()) + 1e-7
