@@ -95,9 +95,9 @@ void launch_rotary(const RotaryParams& p, bool vec, dim3 grid, size_t smem, cuda
     else rotary_kernel<Tin, Tout, false><<<grid, kRotThreads, smem, s>>>(p);
 }
 
-uint64_t mix(uint64_t h, uint64_t x) {  // FNV-1a over the value's bytes
-    for (int i = 0; i < 8; ++i) h = (h ^ ((x >> (8 * i)) & 255)) * 1099511628211ull;
-    return h;
+uint64_t mix(uint64_t h, uint64_t x) {  // a 64-bit value at a time, upper halves folded back
+    h = (h ^ x) * 0x9e3779b97f4a7c15ull;
+    return h ^ (h >> 32);
 }
 
 int heads_of_unit(int group, int nsub) { return (group + nsub - 1) / nsub; }
@@ -155,6 +155,11 @@ lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_he
     for (int a = 0; a < kv_heads; ++a) h = mix(h, uint64_t(sh->dil[a]));
     sh->sig_all = h;
     return LF_OK;
+}
+
+uint64_t workspace_of(const KvShape& sh, int d, int bits) {
+    const int gs = heads_of_unit(sh.q_heads / sh.kv_heads, sh.nsub);
+    return sh.cut ? uint64_t(2) * kv_grid(d, bits, gs) * gs * kv_piece_row(d) * sizeof(float) : 0;
 }
 
 int log2_of(int x) {
@@ -394,10 +399,8 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
 uint64_t lf_attn_cache_workspace_bytes(int n_tokens, int n_global, int page, int max_pages, int q_heads, int kv_heads, int d,
                                        int bits, int r) {
     KvShape sh;
-    if (kv_shape(1, n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, r, nullptr, &sh) != LF_OK || !sh.cut)
-        return 0;
-    const int gs = heads_of_unit(q_heads / kv_heads, sh.nsub);
-    return uint64_t(2) * kv_grid(d, bits, gs) * gs * kv_piece_row(d) * sizeof(float);
+    if (kv_shape(1, n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, r, nullptr, &sh) != LF_OK) return 0;
+    return workspace_of(sh, d, bits);
 }
 
 lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, const void* k_cache, const void* v_cache,
@@ -416,7 +419,7 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     if (!span_of(q, 2, n, strides, d, 2, &a) || !span_of(out, 2, n, strides + 2, d, 2, &b) ||
         !distinct(2, n, strides + 2) || !by_eight(q, 2, strides, 2) || !aligned(out, 2) || a.meets(b))
         return LF_ERR_INVALID_ARG;
-    const uint64_t need = lf_attn_cache_workspace_bytes(n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, r);
+    const uint64_t need = workspace_of(sh, d, bits);
     if (need > 0 && !workspace) return LF_ERR_INVALID_ARG;
     if (workspace_bytes < need) return LF_ERR_SCRATCH_TOO_SMALL;
     if (n_tokens == 0) return LF_OK;

@@ -58,6 +58,7 @@ class KVCache:
             if t is not None and (not t.is_contiguous() or t.device != k.device):
                 raise ValueError("the cache's tensors must be contiguous and on one device")
         self.k, self.v, self.k_par, self.v_par = k, v, k_par, v_par
+        self.shape, self.device_index = (self.kv_heads, self.page, self.d, self.bits), k.get_device()
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, page: int, d: int, dtype: torch.dtype = torch.bfloat16, bits: int = 16,
@@ -100,10 +101,11 @@ class Plan:
         size = lf_attn.load().lf_attn_cache_plan_bytes(S, self.n_tokens, self.n_global)
         if size == 0:
             raise LfAttnError(1, "lf_attn_cache_plan_bytes")
-        self.d, self.bits = cache.d, cache.bits
+        self.d, self.bits, self.shape = cache.d, cache.bits, cache.shape
         self.workspace_bytes = lf_attn.load().lf_attn_cache_workspace_bytes(
             self.n_tokens, self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.d, self.bits,
             self.r)
+        self.device_index = context.get_device()
         self.buffer = _on_stream(stream, context.get_device(), self._inputs(),
                                  lambda raw: torch.empty(size, dtype=torch.uint8, device=context.device))
         self.refresh(stream)
@@ -126,9 +128,10 @@ class Plan:
         return self
 
     def _check(self, cache: KVCache):
-        if cache.kv_heads != self.kv_heads or cache.page != self.page or cache.d != self.d or \
-                cache.bits != self.bits:
+        if cache.shape != self.shape:
             raise ValueError("the plan was made for a cache with other heads, pages or bits")
+        if cache.device_index != self.device_index:
+            raise ValueError("plan and cache must be on one device")
 
 
 def _rows(t: torch.Tensor, n: int, heads: int, d: int, dtype, what: str):
@@ -181,7 +184,9 @@ def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Opti
         for t in held:
             _rows(t, n, hkv, d, dtype, "held")
     rot = _check_freqs(freqs, d)
-    used = (k, v, plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par, q, freqs, q_out, hk, hv)
+    used = (k, v, q, freqs, q_out, hk, hv)
+    if stream is not None:
+        used += (plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par)
 
     def call(raw):
         nonlocal q_out, hk, hv
@@ -203,7 +208,7 @@ def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Opti
                 raise LfAttnError(st, "lf_attn_cache_append")
         return (q_out, hk, hv) if hk is not None else q_out
 
-    return _on_stream(stream, k.get_device(), used, call)
+    return _on_stream(stream, cache.device_index, used, call)
 
 
 def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = None,
@@ -216,7 +221,9 @@ def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = No
     n, heads, d, dtype = plan.n_tokens, plan.q_heads, cache.d, q.dtype
     code = _code(cache, dtype)
     qs = _rows(q, n, heads, d, dtype, "q")
-    used = (q, plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par, out, workspace)
+    used = (q, out, workspace)
+    if stream is not None:
+        used += (plan.buffer, plan.table, cache.k, cache.v, cache.k_par, cache.v_par)
     if out is not None:
         _rows(out, n, heads, d, dtype, "out")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
@@ -238,4 +245,4 @@ def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = No
             raise LfAttnError(st, "lf_attn_cache_fwd")
         return y
 
-    return _on_stream(stream, q.get_device(), used, call)
+    return _on_stream(stream, cache.device_index, used, call)
