@@ -113,27 +113,28 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
             strides += _NONE
             at.append(None)
             continue
-        shape, stride = t.shape, t.stride()
-        if len(shape) != 4:
+        if t.dim() != 4:
             raise ValueError("q, k, v must be [B, heads, T, d]")
-        if shape[0] != B or shape[2] != T or shape[3] != d:
+        (b, h, n, e), (sb, sh, st, se) = t.shape, t.stride()
+        if b != B or n != T or e != d:
             raise ValueError("q, k, v must share B, T and d")
         if t.dtype is not dtype:
             raise TypeError("q, k, v must share a dtype")
-        if stride[3] != 1 and d > 1:
+        if se != 1 and d > 1:
             raise ValueError("the d values of a row must be contiguous")
-        heads.append(shape[1])
-        strides += stride[:3]
+        heads.append(h)
+        strides += (sb, sh, st)
         at.append(t.data_ptr())
     if heads[1] != heads[2] and k is not None and v is not None:
         raise ValueError("k and v must have the same heads")
     rot = _check_freqs(f, d)
     pos_at, pos_stride = None, 0
     if pos is not None:
-        shape = pos.shape
-        if pos.dtype is not torch.int32 or (shape != (B, T) and shape != (T,)) or (T > 1 and pos.stride(-1) != 1):
+        dims = pos.dim()
+        if pos.dtype is not torch.int32 or not 1 <= dims <= 2 or pos.shape[-1] != T or (
+                dims == 2 and pos.shape[0] != B) or (T > 1 and pos.stride(-1) != 1):
             raise ValueError("pos must be an int32 [T] or [B, T] tensor with its last dimension contiguous")
-        if len(shape) == 2:
+        if dims == 2:
             pos_stride = pos.stride(0)
         pos_at = pos.data_ptr()
     if out is None:
@@ -171,7 +172,7 @@ def _turn(q, k, v, f, pos, interleaved, amplitude, out, out_dtype, stream, inver
         else:
             for t in y:
                 strides.extend(_NONE if t is None else t.stride()[:3])
-        if B == 0 or T == 0 or not any(heads):  # nothing to turn: empty tensors have no address
+        if B == 0 or T == 0 or heads == [0, 0, 0]:  # nothing to turn: empty tensors have no address
             return y
         for t in y:
             at.append(None if t is None else t.data_ptr())
