@@ -294,9 +294,10 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  * lf_attn_cache_fwd -- the attention of the step's rows over the cache, which
  * already holds their own keys.  q and out: DEVICE rows
  * [n_tokens][q_heads][d], strides HOST int64 [4]: (token, head) of q, of out;
- * q's rows are 16-byte aligned.  Every row reads its own keys, so this is for
- * single tokens and short drafts; a prompt of thousands is slow here, and where
- * its window may look both ways it belongs to lf_attn_fwd.  workspace: DEVICE,
+ * q's rows are 16-byte aligned.  Up to 16 / (q_heads / kv_heads) consecutive
+ * rows of a sequence (drafts, prompts) share the reading of their keys, unless
+ * dil is above 1; a prompt whose window looks both ways belongs to
+ * lf_attn_fwd.  workspace: DEVICE,
  * lf_attn_cache_workspace_bytes bytes for these sizes (0 where no row's keys
  * are split between CTAs; NULL will do then), 16-byte aligned, of
  * this call alone while it runs.  The plan must have been made with the

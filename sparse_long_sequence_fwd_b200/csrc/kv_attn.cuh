@@ -6,12 +6,21 @@
 // and a key that is not in the set is never loaded (its slot counts as
 // zeros), whatever the cache holds there.
 //
+// kPack: a unit is a tile of consecutive rows of a sequence (drafts, prompts),
+// whose windows differ at the ends.  The keys that all rows see are taken as
+// above; of the others each score is masked by its row's window, and a value
+// that is no number (infinity, NaN) is kept from the rows that do not see it: 0
+// times it is not 0, so then the products are taken row by row, with the row's
+// own keys alone.  (Such a step costs a few times as much; it is rare.)
+//
 // Bound: the cache's bytes.  A key's row is read once for at most 16 query
 // heads, so the intensity is at most 16 flops a byte in 16 bits (measured: 16
 // sequences of 16384 to 32768 tokens, 8 kv heads of 128, bf16: 1.63 GB in 244
-// us, the rate of a plain copy).  Both products are written transposed, S^T = K Q^T and O^T = V^T P^T (m16n8k16 with 16 keys,
-// or 16 value dimensions, as M and 8 query heads as N), which needs half the
-// MMAs and accumulators of the other order when there are few heads.
+// us, the rate of a plain copy; 16 sequences of 4 drafted tokens, 4000 keys, 32
+// heads on 8 of 128: 262 MB in 55 us).  Both products are written transposed,
+// S^T = K Q^T and O^T = V^T P^T (m16n8k16 with 16 keys, or 16 value dimensions,
+// as M and 8 query heads as N), which needs half the MMAs and accumulators of
+// the other order when there are few heads.
 //   lane (g, c) = (lane / 4, lane % 4).  K: the lane reads the 16-byte chunks
 //   c, c + 4, .. of keys g and g + 8; the MMA's k index is a permutation of
 //   the head dimension, the same for Q.  V: chunk g (and g + 8) of keys 2c,
@@ -22,9 +31,9 @@
 // keeps its own running maximum, sum and O, joined through shared memory when
 // the unit's piece ends.  Each warp has a ring of stages in shared memory that
 // it fills itself with cp.async, one block ahead of the one it computes (two
-// ahead measured 4 % slower over long sequences), across unit boundaries too (short windows are a few blocks long); the page
-// table is read one block before that, and the next unit's queries while the
-// last block of a unit is computed.
+// ahead measured 4 % slower over long sequences), across unit boundaries too
+// (short windows are a few blocks long); the page table is read one block before
+// that, and the next unit's queries while the last block of a unit is computed.
 //
 // 4 bits: a group of 32 values is mid + scale (c - 8).  A code or'ed into the
 // mantissa of 1024 is an f16 (1024 + c, or 1024 + 16 c for a nibble four bits
@@ -35,8 +44,7 @@
 // 2^-14 of the largest, and to 2^-25 of it below.  V is made f16 values, one
 // rounding (2^-11).  Bound here: instructions, about 28 a key and warp at d =
 // 128, half of them integer ones to spread nibbles (4 sequences of 32768 to
-// 65536 tokens, 8 kv heads of 128: 264 MB in 82 us, 49 % of the copy rate; 51
-// us with the products left out).
+// 65536 tokens, 8 kv heads of 128: 264 MB in 76 us, 53 % of the copy rate).
 //
 // Rounding: scores, maxima, sums and O in fp32.  P goes to the tensor cores in
 // two bf16 (2^-15) or f16 parts (2^-20): the second part's MMAs are free where
@@ -61,10 +69,14 @@ constexpr int kStages = 2;
 __host__ __device__ constexpr int kv_sub(int bits) { return bits == 16 ? 1 : 2; }
 __host__ __device__ constexpr int kv_block(int bits) { return kKvWarps * 16 * kv_sub(bits); }
 
+// Query rows of a tile, at most.  Over 4 bits of d = 128 16 rows spill (16
+// sequences of 6 drafts, 4000 keys, 32 heads on 8: 109 us against 88 with 8).
+__host__ __device__ constexpr int kv_tile_rows(int d, int bits) { return d == 128 && bits == 4 ? 8 : 16; }
+
 // CTAs of four warps that an SM holds at once, by registers (128 to 255 a
 // thread).
-__host__ __device__ constexpr int kv_ctas_per_sm(int d, int bits, bool two) {
-    return d == 64 ? (two || bits == 4 ? 3 : 4) : (bits == 16 || two ? 2 : 3);
+__host__ __device__ constexpr int kv_ctas_per_sm(int d, int bits, bool two, bool pack) {
+    return pack ? (d == 128 ? 2 : 3) : d == 64 ? (two || bits == 4 ? 3 : 4) : (bits == 16 || two ? 2 : 3);
 }
 
 // A stage: for each 16 keys the K rows, the V rows, and for 4 bits their parameters.
@@ -89,9 +101,10 @@ struct KvAttnParams {
     const int32_t* table;  // [S][max_pages]
     KvPlan plan;
     uint32_t* status;
-    float* part;         // [2 G][heads of a unit][d + 2]
+    float* part;         // [2 G][unit_rows][d + 2]
     int N, n_pages, log_page, max_pages;
     int kv_heads, group, nsub, gs, r, n_global, G;
+    int unit_rows;       // most query rows of a unit: gs times the rows of a tile
     float sl2;           // scale * log2(e)
     uint64_t sig;
     int32_t dil[kMaxHeads];
@@ -284,7 +297,7 @@ __device__ __forceinline__ float2 par_of(uint32_t x) {  // (scale, mid)
 
 // The warp's state of a unit.  Query heads 8 n + 2c and 8 n + 2c + 1 of this
 // lane are columns 0 and 1 of its n-th tile.
-template <int HD, int kBits, bool kHalf, int kNt>
+template <int HD, int kBits, bool kHalf, int kNt, bool kPack>
 struct KvState {
     static constexpr int kGroups = HD / 32;
     static constexpr bool kSplitP = kBits == 4 && kHalf;
@@ -300,16 +313,24 @@ struct KvState {
     float qs[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2], qa[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2];
     float rs[kNt][2];
 
-    // The unit's queries as they are in memory: lane (g, c) takes chunks c, c + 4, .. of query head 8 n + g.
+    // Where query row i of a unit is from its first one on, in elements.
+    static __device__ __forceinline__ int64_t row_at(int i, int gs, int64_t token, int64_t head) {
+        if constexpr (kPack) return (i / gs) * token + (i % gs) * head;
+        else return i * head;
+    }
+
+    // The unit's queries as they are in memory: lane (g, c) takes chunks c, c + 4, .. of query row 8 n + g (heads of a
+    // token, then of the next).
     static __device__ __forceinline__ void load_q(uint4 (&x)[kNt][HD / 32], const KvAttnParams& p, const uint8_t* qrow,
-                                                  int heads, int lane) {
+                                                  int rows, int lane) {
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
         for (int n = 0; n < kNt; ++n)
 #pragma unroll
             for (int j = 0; j < HD / 32; ++j)
-                x[n][j] = 8 * n + g < heads
-                              ? __ldg(reinterpret_cast<const uint4*>(qrow + 2 * p.q_head * (8 * n + g)) + c + 4 * j)
+                x[n][j] = 8 * n + g < rows
+                              ? __ldg(reinterpret_cast<const uint4*>(qrow + 2 * row_at(8 * n + g, p.gs, p.q_row, p.q_head)) +
+                                      c + 4 * j)
                               : make_uint4(0, 0, 0, 0);
     }
 
@@ -482,7 +503,7 @@ struct KvState {
                 }
             }
         } else {
-uint32_t b[kNt][2], b2[kNt][2];
+            uint32_t b[kNt][2], b2[kNt][2];
 #pragma unroll
             for (int n = 0; n < kNt; ++n)
 #pragma unroll
@@ -525,8 +546,115 @@ uint32_t b[kNt][2], b2[kNt][2];
         }
     }
 
-    // One step over a stage; bit i of ok: there is a key i.
-    __device__ __forceinline__ void step(const uint8_t* stage, int g, int c, uint32_t ok) {
+    // The A operands of value tile T (two dimensions of this lane): keys 2c, 2c + 1 beside each other, then 2c + 8, 2c + 9.
+    static __device__ __forceinline__ void value_tile(const KvRegs<HD, kBits>& x, int T, uint32_t (&a)[4]) {
+        if constexpr (kBits == 16) {
+            const int j = T / 4, t = T % 4;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t v0 = (&x.v[2 * i][j].x)[t], v1 = (&x.v[2 * i + 1][j].x)[t];
+                a[2 * i] = __byte_perm(v0, v1, 0x5410);
+                a[2 * i + 1] = __byte_perm(v0, v1, 0x7632);
+            }
+        } else {
+            const int j = T / 2;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t sp = __byte_perm(x.vp[2 * i][j], x.vp[2 * i + 1][j], 0x5410);
+                const uint32_t mp = __byte_perm(x.vp[2 * i][j], x.vp[2 * i + 1][j], 0x7632);
+                uint32_t u = __byte_perm(x.v[2 * i][j / 2], x.v[2 * i + 1][j / 2], (j & 1) ? 0x7632 : 0x5410);
+                if (T & 1) u >>= 8;
+                const __half2 scale = *reinterpret_cast<const __half2*>(&sp), mid = *reinterpret_cast<const __half2*>(&mp);
+                const __half2 lo = __hfma2(code_value<false>(u), scale, mid), up = __hfma2(code_value<true>(u), scale, mid);
+                a[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
+                a[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&up);
+            }
+        }
+    }
+
+    // values() where not every row sees every key: weights of 0 are 0 in both parts, and where there are values that are no
+    // numbers, the products are taken token by token.  key(i): code of key i of these 16 (KvTile::sees).
+    template <typename Tile, typename Key>
+    __device__ __forceinline__ void values_masked(const float (&s)[kNt][4], const uint8_t* sub, int g, int c,
+                                                  const Tile& tile, Key key) {
+        constexpr bool kF16 = kBits == 4 || kHalf, kTwo = kBits == 16 || kSplitP;
+        KvRegs<HD, kBits> x;
+        x.load_v(sub, g, c);
+        uint32_t b[kNt][2], b2[kNt][2];
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float p0 = s[n][2 * i], p1 = s[n][2 * i + 1];
+                uint32_t hi;
+                float2 f;
+                if constexpr (kF16) {
+                    hi = kTwo ? pack_f16x2_rz(p0, p1) : pack_f16x2(p0, p1);
+                    f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                } else {
+                    hi = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+                    f = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+                }
+                b[n][i] = movmatrix_t(hi);
+                constexpr float kTiny = kF16 ? 0x1p-24f : 1e-37f;
+                const float l0 = p0 == 0.f ? 0.f : fmaxf(p0 - f.x, kTiny), l1 = p1 == 0.f ? 0.f : fmaxf(p1 - f.y, kTiny);
+                if constexpr (kTwo) b2[n][i] = movmatrix_t(kF16 ? pack_f16x2(l0, l1) : pack_bf16x2(l0, l1));
+            }
+        constexpr uint32_t kExp = kF16 ? 0x7c007c00u : 0x7f807f80u;
+        bool odd = false;  // an exponent of all ones
+#pragma unroll
+        for (int T = 0; T < HD / 16; ++T) {
+            uint32_t a[4];
+            value_tile(x, T, a);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t e = ~a[i] & kExp;
+                odd |= !(e & 0xffffu) || !(e >> 16);
+            }
+        }
+        if (!__any_sync(~0u, odd)) {
+#pragma unroll
+            for (int T = 0; T < HD / 16; ++T) {
+                uint32_t a[4];
+                value_tile(x, T, a);
+#pragma unroll
+                for (int n = 0; n < kNt; ++n) {
+                    mma16816<kF16>(o[n][T], a[0], a[1], a[2], a[3], b[n][0], b[n][1]);
+                    if constexpr (kTwo) mma16816<kF16>(o[n][T], a[0], a[1], a[2], a[3], b2[n][0], b2[n][1]);
+                }
+            }
+            return;
+        }
+        for (int t = 0; t < tile.rows; ++t) {  // token t's keys alone, into its own columns
+            const int2 see = tile.row(t);
+            uint32_t keep[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k0 = key(2 * c + 8 * i), k1 = key(2 * c + 8 * i + 1);
+                keep[i] = (Tile::sees(see, k0) ? 0xffffu : 0u) | (Tile::sees(see, k1) ? 0xffff0000u : 0u);
+            }
+#pragma unroll
+            for (int T = 0; T < HD / 16; ++T) {
+                uint32_t a[4];
+                value_tile(x, T, a);
+#pragma unroll
+                for (int n = 0; n < kNt; ++n) {
+                    float r[4];
+                    mma16816_first<kF16>(r, a[0] & keep[0], a[1] & keep[0], a[2] & keep[1], a[3] & keep[1], b[n][0], b[n][1]);
+                    if constexpr (kTwo)
+                        mma16816<kF16>(r, a[0] & keep[0], a[1] & keep[0], a[2] & keep[1], a[3] & keep[1], b2[n][0], b2[n][1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if ((8 * n + 2 * c + (i & 1)) / tile.gs == t) o[n][T][i] += r[i];
+                }
+            }
+        }
+    }
+
+    // One step over a stage; bit i of ok: there is a key i.  masked (kPack): not every row sees every key.
+    template <typename Tile>
+    __device__ __forceinline__ void step(const uint8_t* stage, int g, int c, uint32_t ok, bool masked, int code,
+                                         const Tile& tile) {
         constexpr int kSub = KvStage<HD, kBits>::kSub;
         constexpr uint32_t kAll = kSub == 2 ? ~0u : 0xffffu;
         float s[kSub][kNt][4];
@@ -538,7 +666,26 @@ uint32_t b[kNt][2], b2[kNt][2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[u][n][i] *= rs[n][i & 1];
         }
-        if (ok != kAll) {
+        if constexpr (kPack) {
+            if (masked) {
+                int k[kSub][2];
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) k[u][i] = __shfl_sync(~0u, code, 16 * u + 8 * i + g);
+#pragma unroll
+                for (int n = 0; n < kNt; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int2 see = tile.row((8 * n + 2 * c + e) / tile.gs);
+#pragma unroll
+                        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (!Tile::sees(see, k[u][i])) s[u][n][2 * i + e] = -INFINITY;
+                    }
+            }
+        } else if (ok != kAll) {
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -591,6 +738,14 @@ uint32_t b[kNt][2], b2[kNt][2];
                         l[n][e] += s[u][n][i];
                     }
             }
+        if constexpr (kPack)
+            if (masked) {
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+                    values_masked(s[u], stage + u * KvStage<HD, kBits>::kSubBytes, g, c, tile,
+                                  [&](int i) { return __shfl_sync(~0u, code, 16 * u + i); });
+                return;
+            }
 #pragma unroll
         for (int u = 0; u < kSub; ++u) values(s[u], stage + u * KvStage<HD, kBits>::kSubBytes, g, c);
     }
@@ -601,22 +756,38 @@ uint32_t b[kNt][2], b2[kNt][2];
     }
 };
 
+// The rows of a unit's tile and what they see.  A key's code: its position j for
+// one of the window's block, ~j for an entry of the global list, kNoKey for none.
+constexpr int kNoKey = 0x7fffffff;
+struct KvTile {
+    int pos, r, rows, globals, gs;
+    // Row t's window, first and last key; (0, -1) of a row that is none.
+    __device__ __forceinline__ int2 row(int t) const {
+        return t < rows ? make_int2((globals >> t) & 1 ? 0 : max(0, pos + t - r), pos + t) : make_int2(0, -1);
+    }
+    // Window keys of the row's own window, list entries below it.
+    static __device__ __forceinline__ bool sees(int2 row, int code) {
+        return code >= 0 ? code >= row.x && code <= row.y : ~code < row.x;
+    }
+};
+
 // Where a CTA is in its range of the work sequence; all warps walk alike.
-template <int block>
+template <int block, bool kPack>
 struct KvWalk {
-    int row, unit, seq, pos, ng, head;
+    int row, unit, seq, pos, ng, lo, tile, head;
     int b, b1, nb;   // the next block of the unit, and where the CTA's piece of it ends
-    int64_t left;    // blocks of the range from block b on
+    int64_t left;    // of the range from block b on
     KvKeys u;
 
     __device__ __forceinline__ void enter(const KvAttnParams& p) {
         head = unit / p.nsub;
-        u = KvKeys(pos, ng, p.r, p.dil[head]);
+        u = kPack ? KvKeys(lo, pos + (tile & 255) - 1, ng) : KvKeys(pos, ng, p.r, p.dil[head]);
         nb = u.blocks(block);
         b1 = static_cast<int>(min(int64_t(nb), b + left));
     }
     __device__ __forceinline__ KvWalk(const KvAttnParams& p, const KvStart& s)
-        : row(s.row), unit(s.unit), seq(s.seq), pos(s.pos), ng(s.ng), b(s.blk), left(s.n), u(s.pos, s.ng, p.r, 1) {
+        : row(s.row), unit(s.unit), seq(s.seq), pos(s.pos), ng(s.ng), lo(s.lo), tile(s.tile), b(s.blk), left(s.n),
+          u(0, 0, 0) {
         enter(p);
     }
     __device__ __forceinline__ void next_unit(const KvAttnParams& p) {
@@ -624,7 +795,7 @@ struct KvWalk {
         if (++unit == p.kv_heads * p.nsub) {
             unit = 0;
             do ++row;
-            while (row < p.N && p.plan.row_seq[row] < 0);  // rows without keys
+            while (row < p.N && p.plan.row_tile[row] == 0);  // rows that begin no tile
             if (row >= p.N) {
                 left = 0;
                 return;
@@ -632,28 +803,44 @@ struct KvWalk {
             seq = p.plan.row_seq[row];
             pos = p.plan.row_pos[row];
             ng = p.plan.row_ng[row];
+            if constexpr (kPack) {
+                lo = p.plan.row_lo[row];
+                tile = p.plan.row_tile[row];
+            }
         }
+        left -= kUnitKeys / block;
         enter(p);
     }
 
-    // The row of the cache that key i = lane % (keys of a warp) of the warp's part of block b is in, -1: no such key.
-    __device__ __forceinline__ int key_row(const KvAttnParams& p, int warp, int lane) const {
+    // Whether some row does not see some of the warp's keys of block b (kPack).
+    __device__ __forceinline__ bool masked(const KvAttnParams& p, int warp) const {
+        const int n0 = b * block + block / kKvWarps * warp, n1 = n0 + block / kKvWarps, last = pos + (tile & 255) - 1;
+        return n1 > u.n_win || u.first + n1 - 1 > pos || u.first + n0 < max(0, last - p.r);
+    }
+
+    // The row of the cache that key i = lane % (keys of a warp) of the warp's part of block b is in, -1: no such key;
+    // and its code (KvTile).
+    __device__ __forceinline__ int key_row(const KvAttnParams& p, int warp, int lane, int& code) const {
         constexpr int kKeys = block / kKvWarps;
         const int n = b * block + kKeys * warp + (lane & (kKeys - 1));
+        code = kNoKey;
         if (n >= u.n) return -1;
         int at;
         if (n < u.n_win) {
             at = u.first + n * u.step;
         } else {
             at = p.plan.g_list[int64_t(seq) * p.n_global + (n - u.n_win)];
-            const int back = pos - at;  // > 0
-            if (back % u.step == 0 && back / u.step < u.n_win) return -1;  // in the window
+            if constexpr (!kPack) {
+                const int back = pos - at;  // > 0
+                if (back % u.step == 0 && back / u.step < u.n_win) return -1;  // in the window
+            }
         }
         const int page = p.table[int64_t(seq) * p.max_pages + (at >> p.log_page)];
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
             atomicOr(p.status, kStatusBadCache);
             return -1;
         }
+        code = n < u.n_win ? at : ~at;
         return ((page * p.kv_heads + head) << p.log_page) + (at & ((1 << p.log_page) - 1));
     }
 };
@@ -670,22 +857,23 @@ __host__ __device__ constexpr int kv_piece_row(int d) { return d + 2; }
 // The warps' rings, and room to join 8 query heads' 64 dimensions of the four warps at a time.
 constexpr int kJoinRow = 68;
 template <int HD, int kBits>
-constexpr int kv_attn_smem(int gs) {
-    return kKvWarps * (kStages * KvStage<HD, kBits>::kBytes + (gs < 8 ? gs : 8) * kJoinRow * 4);
+constexpr int kv_attn_smem(int unit_rows) {
+    return kKvWarps * (kStages * KvStage<HD, kBits>::kBytes + (unit_rows < 8 ? unit_rows : 8) * kJoinRow * 4);
 }
 
-template <int HD, int kBits, bool kHalf, int kNt>
-__global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2))
+template <int HD, int kBits, bool kHalf, int kNt, bool kPack>
+__global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2, kPack))
     kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
     constexpr int kRows = 8 * kNt;
     constexpr int kStage = KvStage<HD, kBits>::kBytes;
     constexpr int kBlock = kv_block(kBits);
     constexpr int kUnits = 8;  // descriptors in flight: at most kStages + 2 units are between the walk and the end
-    using State = KvState<HD, kBits, kHalf, kNt>;
+    using State = KvState<HD, kBits, kHalf, kNt, kPack>;
     extern __shared__ __align__(128) uint8_t s_ring[];
     float* s_o = reinterpret_cast<float*>(s_ring + kKvWarps * kStages * kStage);
     __shared__ float s_m[kKvWarps][kRows], s_l[kKvWarps][kRows];
-    __shared__ int4 s_unit[kKvWarps][kUnits];  // row, unit, -, slot of its partial state (-1: whole)
+    __shared__ int4 s_unit[kKvWarps][kUnits];  // row, unit, tile, slot of its partial state (-1: whole)
+    __shared__ int s_pos[kKvWarps][kUnits];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int s = blockIdx.x;
     grid_dep_launch();
@@ -699,17 +887,21 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
     const uint32_t ring_at = smem_u32(ring);
 
     // The walk runs ahead of the blocks that are computed.  Of each block in
-    // flight: which of the warp's keys there are, and a note: bit 0 first and
-    // bit 1 last of its piece, from bit 2 the unit's descriptor.
-    KvWalk<kBlock> w(p, start);
+    // flight: which of the warp's keys there are (kPack: their codes), and a
+    // note: bit 0 first and bit 1 last of its piece, bit 2 masked, bits 3 to 5
+    // the unit's descriptor, bit 6 that there is a block.
+    KvWalk<kBlock, kPack> w(p, start);
     int entered = 0;
     auto describe = [&](bool first_piece) {
         const bool whole = w.b == 0 && w.b1 == w.nb;
         // slot 2s: the piece a CTA begins with, of a unit that an earlier one began; 2s + 1: one that a later CTA ends
-        if (lane == 0)
-            s_unit[warp][entered % kUnits] = make_int4(w.row, w.unit, 0, whole ? -1 : 2 * s + (first_piece && w.b > 0 ? 0 : 1));
+        if (lane == 0) {
+            s_unit[warp][entered % kUnits] =
+                make_int4(w.row, w.unit, w.tile, whole ? -1 : 2 * s + (first_piece && w.b > 0 ? 0 : 1));
+            if constexpr (kPack) s_pos[warp][entered % kUnits] = w.pos;
+        }
     };
-    int row_next = -1;
+    int row_next = -1, code_next = kNoKey;
     uint32_t note_next = 0;
     bool fresh = true;
     describe(true);
@@ -717,8 +909,9 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
         row_next = -1;
         note_next = 0;
         if (w.left <= 0) return;
-        row_next = w.key_row(p, warp, lane);
-        note_next = (fresh ? 1u : 0u) | (w.b + 1 == w.b1 ? 2u : 0u) | uint32_t(entered % kUnits) << 2;
+        row_next = w.key_row(p, warp, lane, code_next);
+        note_next = (fresh ? 1u : 0u) | (w.b + 1 == w.b1 ? 2u : 0u) | uint32_t(entered % kUnits) << 3 | 64u;
+        if constexpr (kPack) note_next |= w.masked(p, warp) ? 4u : 0u;
         fresh = false;
         --w.left;
         if (++w.b == w.b1 && w.left > 0) {
@@ -729,12 +922,14 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
         }
     };
     uint32_t ok[kStages], note[kStages];
-    int64_t todo = start.n;
+    int code[kStages];
     auto issue = [&](int stage, int i) {
         kv_issue<HD, kBits>(p, ring_at + stage * kStage, row_next, lane);
         cp_async_commit();
         ok[i] = __ballot_sync(~0u, row_next >= 0) & (kBlock == 64 ? 0xffffu : ~0u);
         note[i] = note_next;
+        code[i] = code_next;
+        if (kPack && ok[i] != (kBlock == 64 ? 0xffffu : ~0u)) note[i] |= 4u;
     };
     fetch();
 #pragma unroll
@@ -743,17 +938,17 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
         fetch();
     }
     auto query = [&](uint4 (&x)[kNt][HD / 32], uint32_t m) {
-        const int4 d = s_unit[warp][m >> 2];
+        const int4 d = s_unit[warp][(m >> 3) & 7];
         const int head = d.y / p.nsub, sub = d.y - head * p.nsub;
         State::load_q(x, p, static_cast<const uint8_t*>(p.q) + 2 * (d.x * p.q_row + (head * p.group + sub * p.gs) * p.q_head),
-                      min(p.gs, p.group - sub * p.gs), lane);
+                      kPack ? (d.z & 255) * p.gs : min(p.gs, p.group - sub * p.gs), lane);
     };
     State st;
     uint4 qn[kNt][HD / 32];
     __syncwarp();
     query(qn, note[0]);
     int stage = 0;
-    for (; todo > 0; --todo) {
+    while (note[0] & 64u) {
         __syncwarp();  // every lane has read the stage that is filled next
         issue(stage == 0 ? kStages - 1 : stage - 1, kStages - 1);
         fetch();
@@ -763,13 +958,19 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
         if (note[1] & 1u) query(qn, note[1]);
         cp_async_wait<kStages - 1>();
         __syncwarp();
-        if (ok[0]) st.step(ring + stage * kStage, g, c, ok[0]);
+        if constexpr (kPack) {
+            const int z = s_unit[warp][(now >> 3) & 7].z;
+            const KvTile tile{s_pos[warp][(now >> 3) & 7], p.r, z & 255, z >> 8, p.gs};
+            if (ok[0]) st.step(ring + stage * kStage, g, c, ok[0], now & 4u, code[0], tile);
+        } else {
+            if (ok[0]) st.step(ring + stage * kStage, g, c, ok[0], false, 0, 0);
+        }
         if (now & 2u) {  // join the lanes' and the warps' states
-            const int4 d = s_unit[warp][now >> 2];
+            const int4 d = s_unit[warp][(now >> 3) & 7];
             const int head = d.y / p.nsub, sub = d.y - head * p.nsub;
-            const int heads = min(p.gs, p.group - sub * p.gs), qh = head * p.group + sub * p.gs;
-            const int join = min(p.gs, 8) * kJoinRow;  // floats of a warp
-            float* part = p.part + int64_t(d.w) * p.gs * kv_piece_row(HD);
+            const int rows = kPack ? (d.z & 255) * p.gs : min(p.gs, p.group - sub * p.gs), qh = head * p.group + sub * p.gs;
+            const int join = min(p.unit_rows, 8) * kJoinRow;  // floats of a warp
+            float* part = p.part + int64_t(d.w) * p.unit_rows * kv_piece_row(HD);
 #pragma unroll
             for (int n = 0; n < kNt; ++n) {
 #pragma unroll
@@ -787,7 +988,7 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
                 for (int half = 0; half < HD / 64; ++half) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if (8 * n + 2 * c + e < heads)
+                        if (8 * n + 2 * c + e < rows)
 #pragma unroll
                             for (int t = 0; t < 4; ++t) {
                                 float* at = s_o + warp * join + (2 * c + e) * kJoinRow;
@@ -795,7 +996,7 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
                                 at[State::dim_of(t, 2, g)] = st.o[n][4 * half + t][2 + e];
                             }
                     __syncthreads();
-                    for (int i = threadIdx.x; i < 64 * min(8, heads - 8 * n); i += kKvThreads) {
+                    for (int i = threadIdx.x; i < 64 * min(8, rows - 8 * n); i += kKvThreads) {
                         const int h = 8 * n + i / 64, e = 64 * half + i % 64;
                         float m = s_m[0][h];
 #pragma unroll
@@ -809,7 +1010,8 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
                             o += s_o[a * join + (i / 64) * kJoinRow + i % 64] * f;
                         }
                         if (d.w < 0) {
-                            store16<kHalf>(p.out, d.x * p.o_row + (qh + h) * p.o_head + e, l == 0.f ? 0.f : o / l);
+                            store16<kHalf>(p.out, d.x * p.o_row + qh * p.o_head + State::row_at(h, p.gs, p.o_row, p.o_head) + e,
+                                           l == 0.f ? 0.f : o / l);
                         } else {
                             float* at = part + h * kv_piece_row(HD);
                             at[e] = o;
@@ -827,6 +1029,7 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
         for (int i = 0; i + 1 < kStages; ++i) {
             ok[i] = ok[i + 1];
             note[i] = note[i + 1];
+            code[i] = code[i + 1];
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
@@ -835,7 +1038,7 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
 
 // Joins the pieces of the unit that CTA s of the attention began and CTA
 // cut.last ended: y = sum of 2^(m_k - M) O_k over sum of 2^(m_k - M) l_k, M =
-// max m_k, in CTA order.  grid: (G, query heads of a unit), HD threads, one
+// max m_k, in CTA order.  grid: (G, query rows of a unit), HD threads, one
 // per dimension; the attention's programmatic dependent.  Bound: latency (all
 // pieces' m and l at once, then their O eight at a time: 6 us with its launch;
 // one piece after the other took 49 us at 12 pieces of 8 heads).  A grid of
@@ -849,10 +1052,12 @@ __global__ void __launch_bounds__(HD) kv_merge_kernel(const __grid_constant__ Kv
     grid_dep_wait();
     if (!mine) return;
     const int head = cut.unit / p.nsub, sub = cut.unit - head * p.nsub;
-    const int heads = min(p.gs, p.group - sub * p.gs), qh = head * p.group + sub * p.gs;
-    if (h >= heads) return;
+    const bool pack = p.unit_rows > p.gs;
+    const int rows = pack ? (cut.tile & 255) * p.gs : min(p.gs, p.group - sub * p.gs), qh = head * p.group + sub * p.gs;
+    if (h >= rows) return;
+    const int64_t at = cut.row * p.o_row + qh * p.o_head + (pack ? h / p.gs * p.o_row + h % p.gs * p.o_head : h * p.o_head);
     // piece 0 is in slot 2s + 1, piece k > 0 in slot 2 (s + k)
-    const int64_t row = kv_piece_row(HD), piece = p.gs * row;
+    const int64_t row = kv_piece_row(HD), piece = p.unit_rows * row;
     const float* base = p.part + 2 * int64_t(s) * piece + h * row;
     const int n = cut.last - s + 1;
     float M = -INFINITY, L = 0.f, O = 0.f;
@@ -892,7 +1097,7 @@ __global__ void __launch_bounds__(HD) kv_merge_kernel(const __grid_constant__ Kv
         for (int i = 0; i < cnt; ++i) L += s_w[i];
         __syncthreads();
     }
-    store16<kHalf>(p.out, cut.row * p.o_row + (qh + h) * p.o_head + e, L == 0.f ? 0.f : O / L);
+    store16<kHalf>(p.out, at + e, L == 0.f ? 0.f : O / L);
 }
 
 }  // namespace lf

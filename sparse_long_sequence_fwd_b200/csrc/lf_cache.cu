@@ -25,7 +25,7 @@ using namespace lf;
 constexpr double kLog2e = 1.4426950408889634;
 // The attention's CTAs: as many as a 148-SM B200 holds at once (larger GPUs run
 // it on as many), so plan and workspace have sizes known without a device.
-int kv_grid(int d, int bits, int gs) { return 148 * kv_ctas_per_sm(d, bits, gs > 8); }
+int kv_grid(int d, int bits, int rows, bool pack) { return 148 * kv_ctas_per_sm(d, bits, rows > 8, pack); }
 static_assert(148 * 4 <= kKvMaxCtas, "");
 constexpr int kMaxRotHeads = 1024;
 constexpr int kAppendSmem = 100 * 1024;
@@ -101,6 +101,7 @@ uint64_t mix(uint64_t h, uint64_t x) {  // a 64-bit value at a time, upper halve
 }
 
 int heads_of_unit(int group, int nsub) { return (group + nsub - 1) / nsub; }
+int unit_rows(const KvShape& sh) { return heads_of_unit(sh.q_heads / sh.kv_heads, sh.nsub) * sh.tpt; }
 
 // Whether units (of up to `keys` keys) are cut between the CTAs.  Whole, the
 // CTAs take ceil(units / grid) rounds of them; cut, units / grid, and a merge
@@ -111,6 +112,40 @@ constexpr int64_t kCutKeys = 320, kLongKeys = 4096;
 bool cut_units(int64_t units, int64_t keys, int64_t grid) {
     const int64_t rounds = (units + grid - 1) / grid;
     return keys > kLongKeys || keys * (rounds * grid - units) > kCutKeys * grid;
+}
+// Tiles are cut for a short last round only where there are few rounds, counted
+// as if every tile were full, so that a workspace's size need not know the
+// sequences: whether tiles of so many rows may be cut at all.
+constexpr int64_t kTileRounds = 4;
+bool may_cut_tiles(int64_t rows, int tpt, int kv_heads, int64_t keys, int64_t grid) {
+    return keys > kLongKeys || (keys > kCutKeys && (rows + tpt - 1) / tpt * kv_heads < kTileRounds * grid);
+}
+
+// Rows of a tile: as many as the sequences have each, up to what a unit holds.
+// Times in us, tiles against single rows: 4096 rows of a prompt, 12 heads of 64,
+// window 256: 83 : 815 (4 bits 95 : 823); 16 sequences of 4 drafts, 4000 keys,
+// 32 heads on 8 of 128: 55 : 153 (4 bits 63 : 100).
+// No tiles where heads are dilated, whose neighbouring rows share no keys.  Not
+// two rows in a unit of 16 either, which costs what two units of 8 do (8
+// sequences of 3, 8000 keys, 16 heads on 2 of 128: 32 against 28).
+int tile_of(const KvShape& sh, int d, int bits) {
+    const int group = sh.q_heads / sh.kv_heads;
+    if (!sh.one_dil || sh.dil[0] != 1 || sh.N < 2 * int64_t(sh.S)) return 1;
+    const int t = static_cast<int>(std::min<int64_t>(kv_tile_rows(d, bits) / group, (int64_t(sh.N) + sh.S - 1) / sh.S));
+    return std::max(1, t * group > 8 && t < 3 ? 8 / group : t);
+}
+
+// How work of tiles of up to tpt rows is split.
+void split_work(KvShape* sh, int d, int bits, int tpt) {
+    sh->tpt = tpt;
+    const int64_t keys = std::min<int64_t>(int64_t(sh->r) + tpt, sh->max_len) + sh->n_global;
+    const int64_t tiles = tpt > 1 ? std::min(sh->N, sh->N / tpt + sh->S) : sh->N;
+    const int64_t blocks = (keys + sh->block - 1) / sh->block, units = tiles * sh->kv_heads * sh->nsub;
+    const int64_t grid = kv_grid(d, bits, unit_rows(*sh), tpt > 1);
+    sh->may_cut = tpt == 1 || may_cut_tiles(sh->N, tpt, sh->kv_heads, keys, grid);
+    sh->cut = sh->may_cut && cut_units(units, keys, grid);
+    // no more CTAs than blocks that ordinary rows can have
+    sh->G = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(grid, blocks * std::min(units, grid))));
 }
 
 lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_heads, int kv_heads, int d, int bits,
@@ -141,25 +176,25 @@ lf_status kv_shape(int S, int N, int n_global, int page, int max_pages, int q_he
         sh->dil[h] = dil ? std::min(dil[h], sh->max_len) : 1;
         if (sh->dil[h] != sh->dil[0]) sh->one_dil = 0;
     }
-    // no more CTAs than blocks that ordinary rows can have
-    const int64_t keys = std::min<int64_t>(int64_t(sh->r) + 1, sh->max_len);
     sh->block = kv_block(bits);
-    const int64_t blocks = (keys + n_global + sh->block - 1) / sh->block, units = int64_t(N) * kv_heads * sh->nsub;
-    const int64_t grid = kv_grid(d, bits, heads_of_unit(group, sh->nsub));
-    sh->cut = cut_units(units, keys + n_global, grid);
-    sh->G = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(grid, blocks * std::min(units, grid))));
+    split_work(sh, d, bits, 1);
+    const int tpt = tile_of(*sh, d, bits);
+    // (whole units of single rows that the CTAs hold at once: tiles are longer; 16 sequences of 2 rows, 12 heads of 64,
+    // window 256: 9.4 us against 8.4)
+    if (tpt > 1 && (sh->cut || int64_t(N) * kv_heads > kv_grid(d, bits, group, false))) split_work(sh, d, bits, tpt);
     uint64_t h = 14695981039346656037ull;
     for (int64_t x : {int64_t(S), int64_t(N), int64_t(page), int64_t(max_pages)}) h = mix(h, uint64_t(x));
     sh->sig_rows = h;
-    for (int64_t x : {int64_t(n_global), int64_t(q_heads), int64_t(kv_heads), int64_t(sh->r), int64_t(d), int64_t(bits)}) h = mix(h, uint64_t(x));
+    for (int64_t x : {int64_t(n_global), int64_t(q_heads), int64_t(kv_heads), int64_t(sh->r), int64_t(d), int64_t(bits),
+                      int64_t(sh->tpt)}) h = mix(h, uint64_t(x));
     for (int a = 0; a < kv_heads; ++a) h = mix(h, uint64_t(sh->dil[a]));
     sh->sig_all = h;
     return LF_OK;
 }
 
 uint64_t workspace_of(const KvShape& sh, int d, int bits) {
-    const int gs = heads_of_unit(sh.q_heads / sh.kv_heads, sh.nsub);
-    return sh.cut ? uint64_t(2) * kv_grid(d, bits, gs) * gs * kv_piece_row(d) * sizeof(float) : 0;
+    const int rows = unit_rows(sh);
+    return sh.cut ? uint64_t(2) * kv_grid(d, bits, rows, sh.tpt > 1) * rows * kv_piece_row(d) * sizeof(float) : 0;
 }
 
 int log2_of(int x) {
@@ -183,10 +218,15 @@ lf_status check_cache(const void* k, const void* v, const void* k_par, const voi
 using AttnKernel = void (*)(KvAttnParams);
 
 template <int HD, int kBits>
-AttnKernel attn_kernel(bool half, int gs, int* smem) {
-    *smem = kv_attn_smem<HD, kBits>(gs);
-    if (half) return gs > 8 ? kv_attn_kernel<HD, kBits, true, 2> : kv_attn_kernel<HD, kBits, true, 1>;
-    return gs > 8 ? kv_attn_kernel<HD, kBits, false, 2> : kv_attn_kernel<HD, kBits, false, 1>;
+AttnKernel attn_kernel(bool half, int unit_rows, bool pack, int* smem) {
+    *smem = kv_attn_smem<HD, kBits>(unit_rows);
+    if (pack) {
+        if constexpr (kv_tile_rows(HD, kBits) > 8)
+            if (unit_rows > 8) return half ? kv_attn_kernel<HD, kBits, true, 2, true> : kv_attn_kernel<HD, kBits, false, 2, true>;
+        return half ? kv_attn_kernel<HD, kBits, true, 1, true> : kv_attn_kernel<HD, kBits, false, 1, true>;
+    }
+    if (unit_rows <= 8) return half ? kv_attn_kernel<HD, kBits, true, 1, false> : kv_attn_kernel<HD, kBits, false, 1, false>;
+    return half ? kv_attn_kernel<HD, kBits, true, 2, false> : kv_attn_kernel<HD, kBits, false, 2, false>;
 }
 
 // Shared-memory limits of the kernels, once per device.
@@ -198,10 +238,13 @@ lf_status kernel_limits() {
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev]) return LF_OK;
     for (int half = 0; half < 2; ++half)
-        for (int gs : {8, 16}) {
+        for (int kind = 0; kind < 4; ++kind) {
+            const int rows = kind & 1 ? 16 : 8;
+            const bool pack = kind & 2;
             int smem[4];
-            const AttnKernel kern[4] = {attn_kernel<64, 16>(half, gs, &smem[0]), attn_kernel<64, 4>(half, gs, &smem[1]),
-                                        attn_kernel<128, 16>(half, gs, &smem[2]), attn_kernel<128, 4>(half, gs, &smem[3])};
+            const AttnKernel kern[4] = {
+                attn_kernel<64, 16>(half, rows, pack, &smem[0]), attn_kernel<64, 4>(half, rows, pack, &smem[1]),
+                attn_kernel<128, 16>(half, rows, pack, &smem[2]), attn_kernel<128, 4>(half, rows, pack, &smem[3])};
             for (int a = 0; a < 4; ++a)
                 if (cudaFuncSetAttribute(kern[a], cudaFuncAttributeMaxDynamicSharedMemorySize, smem[a]) != cudaSuccess ||
                     cudaFuncSetAttribute(kern[a], cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -399,8 +442,16 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
 uint64_t lf_attn_cache_workspace_bytes(int n_tokens, int n_global, int page, int max_pages, int q_heads, int kv_heads, int d,
                                        int bits, int r) {
     KvShape sh;
+    // the most over all numbers of sequences and dilations
     if (kv_shape(1, n_tokens, n_global, page, max_pages, q_heads, kv_heads, d, bits, r, nullptr, &sh) != LF_OK) return 0;
-    return workspace_of(sh, d, bits);
+    const int most = n_tokens < 2 ? 1 : std::max(1, 16 / (q_heads / kv_heads));
+    uint64_t size = 0;
+    for (int t = 1; t <= most; ++t) {
+        split_work(&sh, d, bits, t);
+        if (t > 1) sh.cut = sh.may_cut;
+        size = std::max(size, workspace_of(sh, d, bits));
+    }
+    return size;
 }
 
 lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, const void* k_cache, const void* v_cache,
@@ -449,6 +500,7 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     p.group = q_heads / kv_heads;
     p.nsub = sh.nsub;
     p.gs = heads_of_unit(p.group, p.nsub);
+    p.unit_rows = p.gs * sh.tpt;
     p.r = sh.r;
     p.n_global = n_global;
     p.G = sh.G;
@@ -457,15 +509,18 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     std::memcpy(p.dil, sh.dil, sizeof(p.dil));
     const bool half = dtype == LF_F16;
     int smem = 0;
-    const AttnKernel kern = d == 64 ? (bits == 16 ? attn_kernel<64, 16>(half, p.gs, &smem) : attn_kernel<64, 4>(half, p.gs, &smem))
-                                    : (bits == 16 ? attn_kernel<128, 16>(half, p.gs, &smem) : attn_kernel<128, 4>(half, p.gs, &smem));
+    const bool pack = sh.tpt > 1;
+    const AttnKernel kern = d == 64 ? (bits == 16 ? attn_kernel<64, 16>(half, p.unit_rows, pack, &smem)
+                                                  : attn_kernel<64, 4>(half, p.unit_rows, pack, &smem))
+                                    : (bits == 16 ? attn_kernel<128, 16>(half, p.unit_rows, pack, &smem)
+                                                  : attn_kernel<128, 4>(half, p.unit_rows, pack, &smem));
     kern<<<p.G, kKvThreads, smem, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return LF_ERR_CUDA;
     if (!sh.cut) return LF_OK;
     const AttnKernel merge = d == 64 ? (half ? kv_merge_kernel<64, true> : kv_merge_kernel<64, false>)
                                      : (half ? kv_merge_kernel<128, true> : kv_merge_kernel<128, false>);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.G, p.gs);
+    cfg.gridDim = dim3(p.G, p.unit_rows);
     cfg.blockDim = dim3(d);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

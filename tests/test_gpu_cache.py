@@ -656,3 +656,132 @@ def test_cache_past_32_bit_offsets():
     s.check(kv_cache.fwd(cache, plan, s.q.cuda()))
     kv_cache.append(cache, plan, s.k.cuda(), s.v.cuda())
     assert torch.equal(cache.k[pages - 2, :, 300 - 256].cpu(), s.k[0])
+
+
+PACKED = {  # rows of a sequence that are taken together: dtype, bits, new, old, hq, hkv, d, page, r, dil, globals
+    "two_each": (BF16, 16, [2] * 100, list(range(0, 300, 3)), 4, 4, 64, 16, 30, 1, None),
+    "drafts": (F16, 16, [4, 7, 0, 5] * 12, list(range(300, 348)), 8, 4, 64, 64, 256, 1, [[0, 302, 310]] * 48),
+    "prompt": (BF16, 16, [333], [0], 3, 3, 64, 64, 100, 1, [[0, 40, 41, 200, 332]]),
+    "prompt_behind_one": (F16, 16, [320, 1], [70, 2000], 6, 2, 64, 8, 64, 1, [[0, 64, 65, 69], [0, 1, 2, 1999]]),
+    "window_0": (BF16, 16, [500, 120], [17, 0], 1, 1, 64, 16, 0, 1, [[3, 17, 30], [0, 119, 5]]),
+    "window_1": (F16, 16, [640, 3], [0, 0], 1, 1, 64, 32, 1, 1, None),
+    "many_globals": (BF16, 16, [400, 300], [0, 500], 2, 1, 64, 64, 7, 1, [list(range(0, 400, 2)), list(range(500, 100, -2))]),
+    "shared_3": (BF16, 16, [300, 19], [9, 3], 6, 2, 64, 32, FULL, 1, None),
+    "shared_5_d128": (F16, 16, [200], [130], 10, 2, 128, 64, 60, 1, [[0, 5]]),
+    "shared_4_d128": (BF16, 16, [160, 2], [70, 40], 8, 2, 128, 16, FULL, 1, None),
+    "long": (BF16, 16, [8, 3], [5000, 64], 4, 1, 64, 256, FULL, 1, None),
+    "wide_window": (F16, 16, [4, 2, 4], [3000, 50, 1300], 8, 8, 128, 32, 900, 1, None),
+    "no_tile": (BF16, 16, [600], [100], 2, 2, 64, 16, 20, 2, [[0]]),          # dilated: row by row
+    "four": (BF16, 4, [150, 2], [0, 500], 4, 4, 64, 64, 50, 1, [[0, 30], [0, 3]]),
+    "four_f16": (F16, 4, [5, 3, 9], [100, 1000, 3], 8, 2, 64, 16, FULL, 1, None),
+    "four_d128": (BF16, 4, [4, 4], [3000, 31], 8, 8, 128, 32, FULL, 1, None),
+    "four_f16_d128": (F16, 4, [200], [128], 12, 3, 128, 64, 90, 1, [[0, 128, 164]]),
+}
+
+
+@pytest.mark.parametrize("name", list(PACKED))
+def test_rows_taken_together(name):
+    s = Step(100 + len(name), *PACKED[name]).to_gpu()
+    q = s.q.cuda()
+    got = kv_cache.fwd(s.cache, s.plan, q)
+    s.check(got)
+    s.check(kv_cache.fwd(s.cache, s.plan, q, scale=-0.2), scale=-0.2)
+    assert torch.equal(got, kv_cache.fwd(s.cache, s.plan, q))
+
+
+@pytest.mark.parametrize("dtype,bits,d,hq", [(BF16, 16, 64, 4), (F16, 16, 128, 2), (BF16, 4, 128, 2), (F16, 4, 64, 6)])
+def test_a_row_of_a_tile_does_not_meet_its_neighbours_keys(dtype, bits, d, hq):
+    """No number, in K or in V, at keys that some rows of a tile see: those rows have none, the others are finite and as
+    without it.  Among them list entries: one that rows from 200 on see, one that a whole sequence sees."""
+    for bad in (math.nan, math.inf):
+        for which in (0, 1):
+            s = Step(200, dtype, bits, [300, 5], [0, 50], hq, 2, d, 16, 10, globals_=[[200, 31], [3, 3]], pages_more=0)
+            clean = [None if t is None else t.clone() for t in s.cpu]
+            hit = {(0, j) for j in range(28, 200, 37)} | {(1, 52)} | ({(0, 200), (1, 3)} if which else set())
+            for b, j in hit:
+                at = int(s.table[b, j // 16]), slice(None), j % 16
+                if bits == 16:
+                    s.cpu[which][at] = bad
+                else:
+                    s.cpu[2 + which][at][..., 1] = bad
+            s.to_gpu()
+            got = kv_cache.fwd(s.cache, s.plan, s.q.cuda()).double().cpu()
+            s.cpu = clean
+            want, by, big = ref.attend(s.q, s.cpu, s.table, s.rows, s.r, s.dil, s.globals_, d ** -0.5)
+            tol = ref.attend_tolerance(want, by, big, dtype, bits)
+            for n, (b, p) in enumerate(s.rows):
+                keys = set(ref.key_set(p, 10, 1, s.globals_[b]))
+                if any((b, j) in hit for j in keys):
+                    if which or bad != bad:
+                        assert not torch.isfinite(got[n]).any(), (n, b, p)
+                else:
+                    assert ((got[n] - want[n]).abs() <= tol[n]).all(), (n, b, p)
+
+
+def test_infinite_values_without_weight_in_a_tile():
+    """A value of infinity whose weight is 0 in 64 bits too (scores 80 and -8000: e^-8080): no number in every row that
+    sees it, as 0 times infinity is none, and nothing in the others."""
+    s = Step(201, BF16, 16, [620], [30], 1, 1, 64, 16, 12)
+    s.q.zero_()
+    s.q[:, 0, 0] = 8.0
+    at = int(s.table[0, 2]), 0, 3  # position 35
+    s.cpu[0][:, :, :, 0] = 10.0
+    s.cpu[0][at][0] = -1000.0
+    s.cpu[1][at][5] = math.inf
+    s.to_gpu()
+    got = kv_cache.fwd(s.cache, s.plan, s.q.cuda(), scale=1.0).double().cpu()
+    for n, (_, p) in enumerate(s.rows):
+        assert not torch.isfinite(got[n, 0, 5]) if p - 12 <= 35 <= p else torch.isfinite(got[n]).all(), p
+        assert torch.isfinite(got[n, 0, 6])
+
+
+def test_rows_taken_together_and_bad_pages_tables_and_strides():
+    """Pages outside the cache hold no keys, rows behind the table are none, rows behind the last sequence stay; queries
+    and outputs are rows of wider tensors."""
+    s = Step(202, F16, 16, [280, 21], [40, 10], 4, 2, 64, 16, 25, globals_=[[0, 33], [1, 2]], spare_rows=7)
+    s.table[0, 2], s.table[1, 0] = -5, 1 << 20
+    s.to_gpu()
+    wide = torch.zeros(s.N, 5, 3, 64, dtype=F16, device="cuda")
+    q = wide[:, 1:5, 1]
+    q.copy_(s.q)
+    out = torch.full((s.N, 4, 2, 64), 7.0, dtype=F16, device="cuda")
+    got = kv_cache.fwd(s.cache, s.plan, q, out=out[:, :, 1])
+    assert lf_attn.device_status()[0] & 4
+    s.check(got)
+    assert (out[:, :, 0] == 7).all() and (out[301:] == 7).all()
+
+    s = Step(203, BF16, 16, [304], [40], 2, 2, 64, 16, 25)
+    s.context += 16  # the last 8 rows are behind the table
+    s.rows = [(0, 56 + i) if i < 296 else None for i in range(304)]
+    s.to_gpu()
+    out = torch.full((304, 2, 64), 7.0, dtype=BF16, device="cuda")
+    s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda(), out=out))
+    assert lf_attn.device_status()[0] & 4
+    assert (out[296:] == 7).all()
+
+
+def test_prompt_and_drafts_in_a_captured_step():
+    """A captured step whose sequences take other rows on replay: tiles are made anew."""
+    s = Step(204, BF16, 16, [200, 120], [100, 200], 4, 2, 64, 32, 50, globals_=[[0, 110], [0, 7]]).to_gpu()
+    q, cu, old = s.q.cuda(), s.cu.cuda(), s.context.cuda()
+    table, listed = s.table.cuda(), s.globals_.cuda()
+
+    def step():
+        plan = kv_cache.Plan(s.cache, table, cu, old, s.N, 4, 50, global_idx=listed)
+        return kv_cache.fwd(s.cache, plan, q)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for new, before in (([200, 120], [100, 200]), ([1, 300], [119, 20]), ([290, 0], [10, 5])):
+        cu.copy_(torch.tensor([0, new[0], sum(new)], dtype=torch.int32))
+        old.copy_(torch.tensor(before, dtype=torch.int32))
+        s.rows = [(b, before[b] + i) for b in range(2) for i in range(new[b])]
+        graph.replay()
+        torch.cuda.synchronize()
+        s.check(got)
