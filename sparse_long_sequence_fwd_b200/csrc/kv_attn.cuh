@@ -1,4 +1,4 @@
-// kv_attn.cuh -- attention of single tokens over the paged cache, of 16 or of
+// kv_attn.cuh -- attention of new tokens over the paged cache, of 16 or of
 // 4 bits, and the merge of units that were cut between CTAs.
 //
 // A unit is one token row and the G query heads (at most 8 kNt) that share a

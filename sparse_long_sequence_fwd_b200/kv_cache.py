@@ -1,4 +1,4 @@
-"""The paged key/value cache, of 16 or of 4 bits, and the attention of single tokens over it (``lf_attn_cache_*``).
+"""The paged key/value cache, of 16 or of 4 bits, and the attention of new tokens over it (``lf_attn_cache_*``).
 
 One step of a model that answers token by token:
 
