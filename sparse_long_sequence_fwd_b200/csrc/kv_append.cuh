@@ -41,6 +41,7 @@ struct KvAppendParams {
     const double* freqs;  // null: no turn (rot == 0)
     int N, d, rot, n_pages, log_page, max_pages, inter;
     int log_tile, per;
+    int wide;          // rows of x and y begin at 16-byte boundaries
     float amp;
     uint64_t sig;
 };
@@ -125,10 +126,10 @@ __device__ __forceinline__ void quantise8(uint4 raw, bool is_k, bool on, int cc,
             uint32_t(__half_as_ushort(hs)) | uint32_t(__half_as_ushort(hm)) << 16;
 }
 
-// grid: (tiles of tokens, 1 or 3): with 3 a CTA takes k, v or q only, where
+// kW as in rotary_kernel.  grid: (tiles of tokens, 1 or 3): with 3 a CTA takes k, v or q only, where
 // tiles alone are too few to fill the GPU.  smem: (cos, sin) [tile][cs_stride]; 4 bits: the
 // turned k and v rows [k heads + v heads][tile][d] in 16 bits.
-template <typename T, int kBits, bool kVec>
+template <typename T, int kBits, int kW>
 __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
     extern __shared__ __align__(16) uint8_t s_raw[];
     __shared__ KvSlots sl;
@@ -161,9 +162,10 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
         }
         __syncthreads();
     };
-    // kVec: thread i has item i % per of token i / per % tile, and every step-th head; else value by value
-    const int rest = kVec ? threadIdx.x / p.per : threadIdx.x >> p.log_tile;
-    const int t = kVec ? rest & (tile - 1) : threadIdx.x & (tile - 1);
+    // thread i has item i % per of token i / per % tile, and every step-th head
+    const int rest = threadIdx.x / p.per, t = rest & (tile - 1), group = rest >> p.log_tile, it = threadIdx.x - rest * p.per;
+    const int step = (kRotThreads / p.per) >> p.log_tile;
+    int e0, e1;
     bool live = false;  // a row behind the last sequence stays as it was
     int row = -1;
     // Where head h of w (k, v, q) goes: q to its dense row, k and v to the cache (or to shared memory,
@@ -177,9 +179,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
             else if (row >= 0) dst[0] = reinterpret_cast<T*>(p.cache[w]) + int64_t(row + (h << p.log_page)) * p.d;
         }
     };
-    if constexpr (kVec) {
-        const int group = rest >> p.log_tile, it = threadIdx.x - rest * p.per, step = (kRotThreads / p.per) >> p.log_tile;
-        int e0, e1;
+    if constexpr (kW == 0) {
         item_at(it, p.rot, p.inter, e0, e1);
         float2 cs[8];
 #pragma unroll 1
@@ -211,23 +211,41 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
                 });
         }
     } else {
-        ready();
-        if (t < nt) {
-            live = sl.live[t];
-            row = sl.row[t];
-        }
-        for (int w = w0; w < w1; ++w)
-            for (int i = rest; live && i < p.heads[w] * p.per; i += kRotThreads >> p.log_tile) {
-                const int h = i / p.per, e = i - h * p.per;
-                const T* x = static_cast<const T*>(p.x[w]) + int64_t(n0 + t) * p.xt[w] + int64_t(h) * p.xh[w];
-                const float v = turn_one([&](int f) { return RowIo<T>::load(x + f); }, e, w == 1 ? 0 : p.rot, half,
-                                         p.inter, s_cs + t * stride);
-                T* dst[2];
-                to(w, h, dst);
+        pair_at<kW>(it, p.d, p.rot, p.inter, e0, e1);  // (d is a multiple of 4: e1 is there)
+        const bool turned = kW * it < half;
+        float2 cs[kW];
+#pragma unroll 1
+        for (int w = w0; w < w1; ++w) {
+            if (p.heads[w] == 0) continue;
+            move_pairs<T, kW>(
+                static_cast<const T*>(p.x[w]) + int64_t(n0 + t) * p.xt[w], p.xh[w],
+                group < step && t < nt ? group : p.heads[w], step, p.heads[w], e0, e1,
+                [&] {
+                    if (w > w0) return;  // there are always keys
+                    ready();
+                    if (t < nt) {
+                        live = sl.live[t];
+                        row = sl.row[t];
+                        if (turned)
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (dst[k]) RowIo<T>::store(dst[k] + e, v);
-            }
+                            for (int i = 0; i < kW; ++i) cs[i] = s_cs[t * stride + cs_at(kW * it + i, half)];
+                    }
+                },
+                [&](int h, float(&u)[kW], float(&v)[kW]) {
+                    if (!live) return;
+                    if (w != 1 && turned)
+#pragma unroll
+                        for (int i = 0; i < kW; ++i) turn_pair(u[i], v[i], cs[i]);
+                    T* dst[2];
+                    to(w, h, dst);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (dst[k]) {
+                            store_few<T, kW>(dst[k] + e0, u);
+                            store_few<T, kW>(dst[k] + e1, v);
+                        }
+                });
+        }
     }
     if constexpr (kBits == 4) {
         __syncthreads();
@@ -249,7 +267,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
                     T* y = static_cast<T*>(p.y[w]) + int64_t(n0 + a) * p.yt[w] + int64_t(h) * p.yh[w] + 8 * ch;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) c8[k] = fmaf(scale, c8[k], mid);
-                    if constexpr (kVec) RowIo<T>::store8(y, c8);
+                    if (p.wide) RowIo<T>::store8(y, c8);
                     else
 #pragma unroll
                         for (int k = 0; k < 8; ++k) RowIo<T>::store(y + k, c8[k]);

@@ -76,10 +76,10 @@ bool by_eight(const void* p, int dims, const int64_t* s, size_t es) {
 // twice as many heads a thread took 10.5 and 10.6 us against 8.5.)
 // Where 4-bit rows follow through shared memory, twice as many heads (16384
 // tokens of 32 rows: 47 -> 44 us).
-int log_tile_for(int64_t tokens, int heads, int per, bool staged) {
+int log_tile_for(int64_t tokens, int heads, int d, int per, bool staged) {
     int n = 0;
     while ((2 << n) <= kRotMaxTile && (2 << n) * per <= kRotThreads &&
-           int64_t(2 << n) * per * heads <= int64_t(kRotThreads) * (staged ? 10 : 5) && tokens >= int64_t(2 << n) * 296)
+           int64_t(2 << n) * d * heads <= int64_t(kRotThreads) * (staged ? 160 : 80) && tokens >= int64_t(2 << n) * 296)
         ++n;
     return n;
 }
@@ -90,9 +90,18 @@ int apart(int64_t tiles) { return tiles < 296 ? 3 : 1; }
 bool small(const int64_t* s) { return s[0] <= INT32_MAX && s[1] <= INT32_MAX; }
 
 template <typename Tin, typename Tout>
-void launch_rotary(const RotaryParams& p, bool vec, dim3 grid, size_t smem, cudaStream_t s) {
-    if (vec) rotary_kernel<Tin, Tout, true><<<grid, kRotThreads, smem, s>>>(p);
-    else rotary_kernel<Tin, Tout, false><<<grid, kRotThreads, smem, s>>>(p);
+void launch_rotary(const RotaryParams& p, int kw, dim3 grid, size_t smem, cudaStream_t s) {
+    if (kw == 0) rotary_kernel<Tin, Tout, 0><<<grid, kRotThreads, smem, s>>>(p);
+    else if (kw == 1) rotary_kernel<Tin, Tout, 1><<<grid, kRotThreads, smem, s>>>(p);
+    else rotary_kernel<Tin, Tout, 2><<<grid, kRotThreads, smem, s>>>(p);
+}
+
+// How rows are taken: 0: by items of 16 values, else by pairs, so many at a time.  wide: rows begin at 16-byte
+// boundaries.  (4099 tokens, 36 rows of 64, 24 of them turned, half pairs: 13 us by
+// two, 17 by one; 45 value by value.)
+int turn_kind(bool wide, int d, int rot, bool inter) {
+    if (wide && d % 16 == 0 && (inter || rot % 16 == 0)) return 0;
+    return wide && !inter && rot % 4 == 0 && d % 2 == 0 ? 2 : 1;
 }
 
 uint64_t mix(uint64_t h, uint64_t x) {  // a 64-bit value at a time, upper halves folded back
@@ -229,6 +238,13 @@ AttnKernel attn_kernel(bool half, int unit_rows, bool pack, int* smem) {
     return half ? kv_attn_kernel<HD, kBits, true, 2, false> : kv_attn_kernel<HD, kBits, false, 2, false>;
 }
 
+using AppendKernel = void (*)(KvAppendParams);
+
+template <typename T, int kBits>
+AppendKernel append_kernel(int kw) {
+    return kw == 0 ? kv_append_kernel<T, kBits, 0> : kw == 1 ? kv_append_kernel<T, kBits, 1> : kv_append_kernel<T, kBits, 2>;
+}
+
 // Shared-memory limits of the kernels, once per device.
 lf_status kernel_limits() {
     static std::mutex mu;
@@ -251,10 +267,10 @@ lf_status kernel_limits() {
                                          cudaSharedmemCarveoutMaxShared) != cudaSuccess)
                     return LF_ERR_CUDA;
         }
-    for (auto kern : {kv_append_kernel<__half, 4, true>, kv_append_kernel<__half, 4, false>,
-                      kv_append_kernel<__nv_bfloat16, 4, true>, kv_append_kernel<__nv_bfloat16, 4, false>})
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem) != cudaSuccess)
-            return LF_ERR_CUDA;
+    for (int kw = 0; kw < 3; ++kw)
+        for (const AppendKernel kern : {append_kernel<__half, 4>(kw), append_kernel<__nv_bfloat16, 4>(kw)})
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem) != cudaSuccess)
+                return LF_ERR_CUDA;
     done[dev] = true;
     return LF_OK;
 }
@@ -277,7 +293,7 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
     const size_t ei = size_of(in_dtype), eo = size_of(out_dtype);
     RotaryParams p{};
     Span in[3], out[3];
-    bool vec = d % 16 == 0 && (interleaved ? rot % 8 == 0 : rot % 16 == 0);
+    bool wide = true;
     for (int a = 0; a < 3; ++a) {
         if ((x[a] == nullptr) != (y[a] == nullptr)) return LF_ERR_INVALID_ARG;
         p.heads[a] = x[a] ? (a == 0 ? q_heads : kv_heads) : 0;
@@ -288,7 +304,7 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
         const int64_t* ys = strides + 9 + 3 * a;
         if (!span_of(x[a], 3, n, xs, d, ei, &in[a]) || !span_of(y[a], 3, n, ys, d, eo, &out[a]) || !distinct(3, n, ys))
             return LF_ERR_INVALID_ARG;
-        vec = vec && by_eight(x[a], 3, xs, ei) && by_eight(y[a], 3, ys, eo);
+        wide = wide && by_eight(x[a], 3, xs, ei) && by_eight(y[a], 3, ys, eo);
         p.x[a] = x[a];
         p.y[a] = y[a];
         if (!small(xs + 1) || !small(ys + 1)) return LF_ERR_UNSUPPORTED;
@@ -316,17 +332,18 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
     p.inter = interleaved ? 1 : 0;
     p.back = inverse ? 1 : 0;
     p.amp = amplitude;
-    p.per = vec ? d / 16 : d;
-    p.log_tile = log_tile_for(int64_t(B) * T, heads, p.per, false);
+    const int kw = turn_kind(wide, d, rot, interleaved != 0);
+    p.per = kw == 0 ? d / 16 : pair_items(d, rot, kw);
+    p.log_tile = log_tile_for(int64_t(B) * T, heads, d, p.per, false);
     const unsigned tiles = (T + (1 << p.log_tile) - 1) >> p.log_tile;
     const dim3 grid(tiles, B, apart(int64_t(tiles) * B));
     const size_t smem = (size_t(cs_stride(rot / 2)) << p.log_tile) * sizeof(float2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (in_dtype == LF_F32 && out_dtype == LF_F32) launch_rotary<float, float>(p, vec, grid, smem, s);
-    else if (in_dtype == LF_F32 && out_dtype == LF_BF16) launch_rotary<float, __nv_bfloat16>(p, vec, grid, smem, s);
-    else if (in_dtype == LF_F32) launch_rotary<float, __half>(p, vec, grid, smem, s);
-    else if (in_dtype == LF_BF16) launch_rotary<__nv_bfloat16, __nv_bfloat16>(p, vec, grid, smem, s);
-    else launch_rotary<__half, __half>(p, vec, grid, smem, s);
+    if (in_dtype == LF_F32 && out_dtype == LF_F32) launch_rotary<float, float>(p, kw, grid, smem, s);
+    else if (in_dtype == LF_F32 && out_dtype == LF_BF16) launch_rotary<float, __nv_bfloat16>(p, kw, grid, smem, s);
+    else if (in_dtype == LF_F32) launch_rotary<float, __half>(p, kw, grid, smem, s);
+    else if (in_dtype == LF_BF16) launch_rotary<__nv_bfloat16, __nv_bfloat16>(p, kw, grid, smem, s);
+    else launch_rotary<__half, __half>(p, kw, grid, smem, s);
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
 }
 
@@ -375,7 +392,7 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     const void* x[3] = {k, v, q};
     void* y[3] = {k_held, v_held, q_out};
     Span in[3], out[3];
-    bool vec = interleaved ? rot % 8 == 0 : rot % 16 == 0;
+    bool wide = true;
     for (int a = 0; a < 3; ++a) {
         p.heads[a] = a < 2 ? kv_heads : (q ? q_heads : 0);
         const int64_t n[2] = {n_tokens, p.heads[a]};
@@ -386,7 +403,7 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
             if (!small(xs)) return LF_ERR_UNSUPPORTED;
             p.xt[a] = static_cast<int>(xs[0]);
             p.xh[a] = static_cast<int>(xs[1]);
-            vec = vec && by_eight(x[a], 2, xs, 2);
+            wide = wide && by_eight(x[a], 2, xs, 2);
         }
         if (y[a]) {
             if (!aligned(y[a], 2) || !span_of(y[a], 2, n, ys, d, 2, &out[a]) || !distinct(2, n, ys))
@@ -394,7 +411,7 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
             if (!small(ys)) return LF_ERR_UNSUPPORTED;
             p.yt[a] = static_cast<int>(ys[0]);
             p.yh[a] = static_cast<int>(ys[1]);
-            vec = vec && by_eight(y[a], 2, ys, 2);
+            wide = wide && by_eight(y[a], 2, ys, 2);
         }
         p.x[a] = x[a];
         p.y[a] = y[a];
@@ -422,19 +439,17 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     p.inter = interleaved ? 1 : 0;
     p.amp = amplitude;
     p.sig = sh.sig_rows;
-    p.per = vec ? d / 16 : d;
-    p.log_tile = log_tile_for(n_tokens, 2 * kv_heads + p.heads[2], p.per, bits == 4);
+    const int kw = turn_kind(wide, d, rot, interleaved != 0);
+    p.per = kw == 0 ? d / 16 : pair_items(d, rot, kw);
+    p.log_tile = log_tile_for(n_tokens, 2 * kv_heads + p.heads[2], d, p.per, bits == 4);
     const size_t staged = bits == 4 ? size_t(2) * kv_heads * d * 2 : 0;  // per token
     const size_t smem = (size_t(cs_stride(rot / 2)) * sizeof(float2) + staged) << p.log_tile;
     const unsigned tiles = (n_tokens + (1 << p.log_tile) - 1) >> p.log_tile;
     const dim3 grid(tiles, apart(tiles));
-    void (*kern)(KvAppendParams);
-    if (dtype == LF_F16)
-        kern = bits == 16 ? (vec ? kv_append_kernel<__half, 16, true> : kv_append_kernel<__half, 16, false>)
-                          : (vec ? kv_append_kernel<__half, 4, true> : kv_append_kernel<__half, 4, false>);
-    else
-        kern = bits == 16 ? (vec ? kv_append_kernel<__nv_bfloat16, 16, true> : kv_append_kernel<__nv_bfloat16, 16, false>)
-                          : (vec ? kv_append_kernel<__nv_bfloat16, 4, true> : kv_append_kernel<__nv_bfloat16, 4, false>);
+    p.wide = wide ? 1 : 0;
+    const AppendKernel kern = dtype == LF_F16 ? (bits == 16 ? append_kernel<__half, 16>(kw) : append_kernel<__half, 4>(kw))
+                                              : (bits == 16 ? append_kernel<__nv_bfloat16, 16>(kw)
+                                                            : append_kernel<__nv_bfloat16, 4>(kw));
     kern<<<grid, kRotThreads, smem, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
 }

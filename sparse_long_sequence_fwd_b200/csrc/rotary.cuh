@@ -21,7 +21,11 @@
 // eight (cos, sin) are read once, and a head costs an address and two wide
 // loads and stores.  Its first kRotItems heads' loads are under way while the
 // CTA computes the sines (one per thread, for all heads), into shared memory
-// in an order in which a warp's reads meet every bank once.
+// in an order in which a warp's reads meet every bank once.  Rows that 16-value
+// items do not divide (half pairs with rot not a multiple of 16, strides or
+// addresses off 16 bytes) are taken in the same way by pairs, two at a time
+// where rot / 2 is even and all is aligned: a thread has its pairs of a row, with
+// their (cos, sin), in every so-many-th head.
 #pragma once
 #include "lf_common.cuh"
 #include "ptx.cuh"
@@ -145,27 +149,73 @@ __device__ __forceinline__ void turn_item(float (&a)[8], float (&b)[8], int it, 
             for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], cs[i]);
         }
     } else {
-        if (16 * it < rot) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) turn_pair(a[2 * i], a[2 * i + 1], cs[i]);
-        }
-        if (16 * it + 8 < rot) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) turn_pair(b[2 * i], b[2 * i + 1], cs[4 + i]);
+        for (int i = 0; i < 4; ++i) {
+            if (16 * it + 2 * i < rot) turn_pair(a[2 * i], a[2 * i + 1], cs[i]);
+            if (16 * it + 2 * i + 8 < rot) turn_pair(b[2 * i], b[2 * i + 1], cs[4 + i]);
         }
     }
 }
 
-// Value e of a row whose value f is at(f), turned (the element-wise path:
-// head dimensions, rot or strides that the 16-value items do not divide).
-template <typename At>
-__device__ __forceinline__ float turn_one(At at, int e, int rot, int half, bool inter, const float2* cs) {
-    const float x = at(e);
-    if (e >= rot) return x;
-    const bool first = inter ? !(e & 1) : e < half;
-    const float2 c = cs[cs_at(inter ? e >> 1 : (first ? e : e - half), half)];
-    const float y = at(inter ? e ^ 1 : (first ? e + half : e - half));
-    return first ? x * c.x - y * c.y : x * c.x + y * c.y;
+// A row by pairs, kW at a time: rot / 2 pairs that are turned, then the others,
+// neighbours.  Item `it`'s kW first and kW second values; e1 < 0 where the
+// row ends before the second ones.
+__host__ __device__ constexpr int pair_items(int d, int rot, int kw) { return (rot / 2 + (d - rot + 1) / 2 + kw - 1) / kw; }
+template <int kW>
+__device__ __forceinline__ void pair_at(int it, int d, int rot, bool inter, int& e0, int& e1) {
+    const bool split = !inter && kW * it < rot / 2;
+    e0 = split ? kW * it : 2 * kW * it;
+    e1 = split ? kW * it + rot / 2 : 2 * kW * it + kW < d ? 2 * kW * it + kW : -1;
+}
+
+// kW neighbouring values of a row.
+template <typename T, int kW>
+struct __align__(kW * sizeof(T)) Few {
+    T v[kW];
+};
+
+// move_rows for pairs; some heads at a time (six: the case of turn_kind's comment 13 us, eight: 17).
+template <typename T, int kW, typename Ready, typename Sink>
+__device__ __forceinline__ void move_pairs(const T* x, int stride, int first, int step, int heads, int e0, int e1,
+                                           Ready ready, Sink sink) {
+    constexpr int kHeads = kW * sizeof(T) > 4 ? 4 : 6;
+    using Word = Few<T, kW>;
+    bool fresh = true;
+    do {
+        Word raw[kHeads][2];
+#pragma unroll
+        for (int a = 0; a < kHeads; ++a) {
+            const int h = first + a * step;
+            if (h < heads) {
+                const T* row = x + int64_t(h) * stride;
+                raw[a][0] = *reinterpret_cast<const Word*>(row + e0);
+                raw[a][1] = *reinterpret_cast<const Word*>(row + (e1 < 0 ? e0 : e1));
+            }
+        }
+        if (fresh) ready();
+        fresh = false;
+#pragma unroll
+        for (int a = 0; a < kHeads; ++a) {
+            const int h = first + a * step;
+            if (h < heads) {
+                float u[kW], v[kW];
+#pragma unroll
+                for (int i = 0; i < kW; ++i) {
+                    u[i] = RowIo<T>::load(&raw[a][0].v[i]);
+                    v[i] = RowIo<T>::load(&raw[a][1].v[i]);
+                }
+                sink(h, u, v);
+            }
+        }
+        first += kHeads * step;
+    } while (first < heads);
+}
+template <typename T, int kW>
+__device__ __forceinline__ void store_few(T* at, const float (&u)[kW]) {
+    Few<T, kW> w;
+#pragma unroll
+    for (int i = 0; i < kW; ++i) RowIo<T>::store(&w.v[i], u[i]);
+    *reinterpret_cast<Few<T, kW>*>(at) = w;
 }
 
 // A thread's item (16 values at e0 and e1 of a row) of heads first, first +
@@ -229,14 +279,15 @@ struct RotaryParams {
     int64_t pos_stride;
     const double* freqs;
     int B, T, d, rot;
-    int log_tile, per;  // tokens per CTA; items (kVec) or values per row
+    int log_tile, per;  // tokens per CTA; items per row
     int inter, back;
     float amp;
 };
 
+// kW: 0: items of 16 values, else pairs, kW at a time.
 // grid: (tiles of tokens, B, 1 or 3): with 3 a CTA takes q, k or v only, where
 // tiles alone are too few to fill the GPU.
-template <typename Tin, typename Tout, bool kVec>
+template <typename Tin, typename Tout, int kW>
 __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotary_kernel(const __grid_constant__ RotaryParams p) {
     extern __shared__ __align__(16) float2 s_cs[];  // [tile][cs_stride]
     const int b = blockIdx.y, tile = 1 << p.log_tile, t0 = blockIdx.x * tile;
@@ -250,15 +301,14 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotary_kernel(const __g
         }
         __syncthreads();
     };
-    // kVec: thread i has item i % per of token i / per % tile, and every step-th head; else value by value
-    const int rest = kVec ? threadIdx.x / p.per : threadIdx.x >> p.log_tile;
-    const int t = kVec ? rest & (tile - 1) : threadIdx.x & (tile - 1);
-    if constexpr (kVec) {
-        const int group = rest >> p.log_tile, it = threadIdx.x - rest * p.per, step = (kRotThreads / p.per) >> p.log_tile;
-        int e0, e1;
+    // thread i has item i % per of token i / per % tile, and every step-th head
+    const int rest = threadIdx.x / p.per, t = rest & (tile - 1), group = rest >> p.log_tile, it = threadIdx.x - rest * p.per;
+    const int step = (kRotThreads / p.per) >> p.log_tile;
+    int e0, e1;
+    bool fresh = true;
+    if constexpr (kW == 0) {
         item_at(it, p.rot, p.inter, e0, e1);
         float2 cs[8];
-        bool fresh = true;
 #pragma unroll 1
         for (int w = w0; w < w1; ++w) {
             if (p.heads[w] == 0) continue;
@@ -281,17 +331,33 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotary_kernel(const __g
                 });
         }
     } else {
-        ready();
+        pair_at<kW>(it, p.d, p.rot, p.inter, e0, e1);
+        const bool turned = kW * it < half;
+        float2 cs[kW];
+#pragma unroll 1
         for (int w = w0; w < w1; ++w) {
+            if (p.heads[w] == 0) continue;
             const Tin* x = static_cast<const Tin*>(p.x[w]) + b * p.xb[w] + int64_t(t0 + t) * p.xt[w];
             Tout* y = static_cast<Tout*>(p.y[w]) + b * p.yb[w] + int64_t(t0 + t) * p.yt[w];
-            for (int i = rest; t < nt && i < p.heads[w] * p.per; i += kRotThreads >> p.log_tile) {
-                const int h = i / p.per, e = i - h * p.per;
-                const Tin* row = x + int64_t(h) * p.xh[w];
-                RowIo<Tout>::store(y + int64_t(h) * p.yh[w] + e,
-                                   turn_one([&](int f) { return RowIo<Tin>::load(row + f); }, e, w == 2 ? 0 : p.rot, half,
-                                            p.inter, s_cs + t * stride));
-            }
+            const int yh = p.yh[w];
+            move_pairs<Tin, kW>(
+                x, p.xh[w], group < step && t < nt ? group : p.heads[w], step, p.heads[w], e0, e1,
+                [&] {
+                    if (!fresh) return;
+                    fresh = false;
+                    ready();
+                    if (turned && t < nt)
+#pragma unroll
+                        for (int i = 0; i < kW; ++i) cs[i] = s_cs[t * stride + cs_at(kW * it + i, half)];
+                },
+                [&](int h, float(&u)[kW], float(&v)[kW]) {
+                    if (w < 2 && turned)
+#pragma unroll
+                        for (int i = 0; i < kW; ++i) turn_pair(u[i], v[i], cs[i]);
+                    Tout* row = y + int64_t(h) * yh;
+                    store_few<Tout, kW>(row + e0, u);
+                    if (e1 >= 0) store_few<Tout, kW>(row + e1, v);
+                });
         }
     }
 }

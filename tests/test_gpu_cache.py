@@ -785,3 +785,52 @@ def test_prompt_and_drafts_in_a_captured_step():
         graph.replay()
         torch.cuda.synchronize()
         s.check(got)
+
+
+# ---------------------------------------------------------------- rows that 16-value items do not divide
+
+PARTS = [  # rotary: B, T, hq, hkv, d, rot, interleaved, in, out
+    (1, 40, 3, 2, 64, 2, False, BF16, BF16),
+    (2, 301, 12, 4, 64, 24, False, BF16, BF16),    # two pairs at a time
+    (1, 77, 5, 5, 64, 62, False, F16, F16),        # one
+    (1, 33, 9, 1, 128, 100, False, F32, BF16),
+    (3, 19, 17, 1, 128, 90, False, F32, F32),
+    (2, 50, 40, 8, 128, 60, True, BF16, BF16),     # rot ends inside a chunk
+    (1, 64, 2, 2, 64, 2, True, F32, F16),
+    (1, 21, 3, 3, 96, 70, True, BF16, BF16),
+    (1, 700, 2, 1, 256, 252, False, F16, F16),
+    (1, 5, 2, 1, 255, 254, False, F32, F32),       # 127 pairs and one value
+    (2, 9, 1, 1, 1, 0, False, BF16, BF16),
+]
+
+
+@pytest.mark.parametrize("case", PARTS, ids=lambda c: "-".join(str(x) for x in c[:7]))
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rotary_rows_by_pairs(case, inverse):
+    test_rotary_rows(case, inverse)
+
+
+@pytest.mark.parametrize("case", [  # dtype, bits, new, old, hq, hkv, d, page, rot, interleaved
+    (BF16, 16, [40, 3], [0, 9], 12, 4, 64, 16, 24, False),
+    (F16, 16, [1, 9], [60, 0], 6, 2, 64, 8, 62, False),
+    (F16, 16, [130], [7], 2, 2, 128, 64, 52, True),
+    (BF16, 4, [33, 2], [0, 77], 4, 4, 64, 32, 24, False),
+    (F16, 4, [17], [20], 8, 1, 128, 16, 90, False),
+    (BF16, 4, [5, 600], [20, 0], 5, 5, 128, 16, 100, False),
+    (F16, 4, [6], [0], 3, 3, 64, 8, 2, True),
+], ids=lambda c: "-".join(str(x) for x in c[1:]))
+def test_append_by_pairs(case):
+    test_append(case)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rot", [2, 12, 22, 36, 60])
+def test_values_behind_rot_are_copies(inter, rot):
+    """Infinities and NaN behind rot stay what they are and where they are."""
+    g = gen(300 + rot)
+    x = torch.randn(1, 3, 50, 64, generator=g)
+    x[..., rot:] = torch.tensor([math.inf, -math.inf, math.nan, 1.5])[torch.randint(0, 4, (1, 3, 50, 64 - rot), generator=g)]
+    x = x.to(BF16).cuda()
+    got = rotary.fwd(x, freqs=rotary.freqs(rot, device="cuda"), interleaved=inter)[0]
+    assert torch.isfinite(got[..., :rot]).all()
+    assert torch.equal(got[..., rot:].nan_to_num(9.0), x[..., rot:].nan_to_num(9.0))
