@@ -17,7 +17,7 @@
 // heads, so the intensity is at most 16 flops a byte in 16 bits (measured: 16
 // sequences of 16384 to 32768 tokens, 8 kv heads of 128, bf16: 1.63 GB in 244
 // us, the rate of a plain copy; 16 sequences of 4 drafted tokens, 4000 keys, 32
-// heads on 8 of 128: 262 MB in 55 us).  Both products are written transposed,
+// heads on 8 of 128: 262 MB in 53 us).  Both products are written transposed,
 // S^T = K Q^T and O^T = V^T P^T (m16n8k16 with 16 keys, or 16 value dimensions,
 // as M and 8 query heads as N), which needs half the MMAs and accumulators of
 // the other order when there are few heads.
@@ -44,7 +44,7 @@
 // 2^-14 of the largest, and to 2^-25 of it below.  V is made f16 values, one
 // rounding (2^-11).  Bound here: instructions, about 28 a key and warp at d =
 // 128, half of them integer ones to spread nibbles (4 sequences of 32768 to
-// 65536 tokens, 8 kv heads of 128: 264 MB in 76 us, 53 % of the copy rate).
+// 65536 tokens, 8 kv heads of 128: 264 MB in 77 us, 52 % of the copy rate).
 //
 // Rounding: scores, maxima, sums and O in fp32.  P goes to the tensor cores in
 // two bf16 (2^-15) or f16 parts (2^-20): the second part's MMAs are free where
@@ -101,9 +101,10 @@ struct KvAttnParams {
     const int32_t* table;  // [S][max_pages]
     KvPlan plan;
     uint32_t* status;
-    float* part;         // [2 G][unit_rows][d + 2]
+    float* part;         // [2 G][unit_rows][d + 4]
     int N, n_pages, log_page, max_pages;
     int kv_heads, group, nsub, gs, r, n_global, G;
+    int o_wide;          // output rows begin at 8-byte boundaries
     int unit_rows;       // most query rows of a unit: gs times the rows of a tile
     float sl2;           // scale * log2(e)
     uint64_t sig;
@@ -307,7 +308,7 @@ struct KvState {
     static constexpr float kLift = kHalfP ? 11.f : 0.f, kRoom = kHalfP ? 4.f : 8.f;
     uint32_t q[kNt][HD / 16][2];
     float o[kNt][HD / 16][4];
-    float m[kNt][2], l[kNt][2];
+    float m[kNt][2], l[kNt][2];  // (o[.][4 j + t][i]: dimension 64 j + 8 g + 2 t + (i >> 1); 4 bits: [2 j + t]: 32 j + 4 g + ..)
     // 4 bits: sums of the scaled q over a group, minus what the codes' 1024 + 8 adds to its products, and the scale of
     // scores (16 bits: the caller's)
     float qs[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2], qa[kBits == 4 ? kNt : 1][kBits == 4 ? kGroups : 1][2];
@@ -749,11 +750,6 @@ struct KvState {
 #pragma unroll
         for (int u = 0; u < kSub; ++u) values(s[u], stage + u * KvStage<HD, kBits>::kSubBytes, g, c);
     }
-
-    // The dimension of o[.][t][i] in this lane.
-    static __device__ __forceinline__ int dim_of(int t, int i, int g) {
-        return kBits == 16 ? 64 * (t / 4) + 8 * g + 2 * (t % 4) + (i >> 1) : 32 * (t / 2) + 4 * g + 2 * (t % 2) + (i >> 1);
-    }
 };
 
 // The rows of a unit's tile and what they see.  A key's code: its position j for
@@ -851,10 +847,11 @@ __device__ __forceinline__ void store16(void* at, int64_t i, float x) {
     else static_cast<__nv_bfloat16*>(at)[i] = __float2bfloat16_rn(x);
 }
 
-// Floats of a partial state: O, m and l of each query head of a unit.
-__host__ __device__ constexpr int kv_piece_row(int d) { return d + 2; }
+// Floats of a partial state: O, m and l of each query row of a unit, in whole 16 bytes.
+__host__ __device__ constexpr int kv_piece_row(int d) { return d + 4; }
 
-// The warps' rings, and room to join 8 query heads' 64 dimensions of the four warps at a time.
+// The warps' rings, and room to join 8 query rows' 64 dimensions of the four warps at a time: a row of 68 floats, so
+// that the 16-byte stores of eight lanes (four rows, two places) meet all banks.
 constexpr int kJoinRow = 68;
 template <int HD, int kBits>
 constexpr int kv_attn_smem(int unit_rows) {
@@ -988,34 +985,61 @@ __global__ void __launch_bounds__(kKvThreads, kv_ctas_per_sm(HD, kBits, kNt == 2
                 for (int half = 0; half < HD / 64; ++half) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if (8 * n + 2 * c + e < rows)
+                        if (8 * n + 2 * c + e < rows) {
+                            float* at = s_o + warp * join + (2 * c + e) * kJoinRow;
+                            float4 x[2];
 #pragma unroll
-                            for (int t = 0; t < 4; ++t) {
-                                float* at = s_o + warp * join + (2 * c + e) * kJoinRow;
-                                at[State::dim_of(t, 0, g)] = st.o[n][4 * half + t][e];
-                                at[State::dim_of(t, 2, g)] = st.o[n][4 * half + t][2 + e];
+                            for (int k = 0; k < 2; ++k)
+                                x[k] = make_float4(st.o[n][4 * half + 2 * k][e], st.o[n][4 * half + 2 * k][2 + e],
+                                                   st.o[n][4 * half + 2 * k + 1][e], st.o[n][4 * half + 2 * k + 1][2 + e]);
+                            if constexpr (kBits == 16) {  // odd g in the other order: eight lanes meet all banks
+                                const bool odd = g & 1;
+                                *reinterpret_cast<float4*>(at + 8 * g + (odd ? 4 : 0)) = odd ? x[1] : x[0];
+                                *reinterpret_cast<float4*>(at + 8 * g + (odd ? 0 : 4)) = odd ? x[0] : x[1];
+                            } else {
+                                *reinterpret_cast<float4*>(at + 4 * g) = x[0];
+                                *reinterpret_cast<float4*>(at + 32 + 4 * g) = x[1];
                             }
+                        }
                     __syncthreads();
-                    for (int i = threadIdx.x; i < 64 * min(8, rows - 8 * n); i += kKvThreads) {
-                        const int h = 8 * n + i / 64, e = 64 * half + i % 64;
+                    // a thread takes four dimensions of a row (once; as a loop the blocks' code comes out 3 % faster)
+                    for (int i = threadIdx.x; i < 16 * min(8, rows - 8 * n); i += kKvThreads) {
+                        const int r = i / 16, h = 8 * n + r, e = 4 * (i % 16);
                         float m = s_m[0][h];
 #pragma unroll
                         for (int a = 1; a < kKvWarps; ++a) m = fmaxf(m, s_m[a][h]);
-                        float l = 0.f, o = 0.f;
+                        float l = 0.f;
+                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int a = 0; a < kKvWarps; ++a) {
                             // a warp without keys has m = -inf and zeros
                             const float f = s_m[a][h] == m ? 1.f : ex2_approx(s_m[a][h] - m);
+                            const float4 y = *reinterpret_cast<const float4*>(s_o + a * join + r * kJoinRow + e);
                             l += s_l[a][h] * f;
-                            o += s_o[a * join + (i / 64) * kJoinRow + i % 64] * f;
+                            o.x += y.x * f;
+                            o.y += y.y * f;
+                            o.z += y.z * f;
+                            o.w += y.w * f;
                         }
                         if (d.w < 0) {
-                            store16<kHalf>(p.out, d.x * p.o_row + qh * p.o_head + State::row_at(h, p.gs, p.o_row, p.o_head) + e,
-                                           l == 0.f ? 0.f : o / l);
+                            const int64_t at = d.x * p.o_row + qh * p.o_head + State::row_at(h, p.gs, p.o_row, p.o_head) +
+                                               64 * half + e;
+                            const float inv = l == 0.f ? 0.f : 1.f / l;
+                            o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                            if (p.o_wide) {
+                                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                                    kHalf ? make_uint2(pack_f16x2(o.x, o.y), pack_f16x2(o.z, o.w))
+                                          : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+                            } else {
+                                store16<kHalf>(p.out, at, o.x);
+                                store16<kHalf>(p.out, at + 1, o.y);
+                                store16<kHalf>(p.out, at + 2, o.z);
+                                store16<kHalf>(p.out, at + 3, o.w);
+                            }
                         } else {
                             float* at = part + h * kv_piece_row(HD);
-                            at[e] = o;
-                            if (e == 0) {
+                            *reinterpret_cast<float4*>(at + 64 * half + e) = o;
+                            if (half == 0 && e == 0) {
                                 at[HD] = m;
                                 at[HD + 1] = l;
                             }

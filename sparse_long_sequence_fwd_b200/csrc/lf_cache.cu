@@ -132,8 +132,8 @@ bool may_cut_tiles(int64_t rows, int tpt, int kv_heads, int64_t keys, int64_t gr
 
 // Rows of a tile: as many as the sequences have each, up to what a unit holds.
 // Times in us, tiles against single rows: 4096 rows of a prompt, 12 heads of 64,
-// window 256: 83 : 815 (4 bits 95 : 823); 16 sequences of 4 drafts, 4000 keys,
-// 32 heads on 8 of 128: 55 : 153 (4 bits 63 : 100).
+// window 256: 71 : 815 (4 bits 83 : 823); 16 sequences of 4 drafts, 4000 keys,
+// 32 heads on 8 of 128: 53 : 153 (4 bits 62 : 100).
 // No tiles where heads are dilated, whose neighbouring rows share no keys.  Not
 // two rows in a unit of 16 either, which costs what two units of 8 do (8
 // sequences of 3, 8000 keys, 16 heads on 2 of 128: 32 against 28).
@@ -498,6 +498,7 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     p.out = out;
     p.q_row = strides[0];
     p.q_head = strides[1];
+    p.o_wide = aligned(out, 8) && strides[2] % 4 == 0 && strides[3] % 4 == 0;
     p.o_row = strides[2];
     p.o_head = strides[3];
     p.k = static_cast<const uint8_t*>(k_cache);

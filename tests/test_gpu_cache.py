@@ -834,3 +834,15 @@ def test_values_behind_rot_are_copies(inter, rot):
     got = rotary.fwd(x, freqs=rotary.freqs(rot, device="cuda"), interleaved=inter)[0]
     assert torch.isfinite(got[..., :rot]).all()
     assert torch.equal(got[..., rot:].nan_to_num(9.0), x[..., rot:].nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("shift", [0, 1, 2, 4])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_outputs_at_any_place(bits, shift):
+    """Outputs whose rows begin on 2, 4 and 8 bytes, of whole units and of cut ones, single rows and tiles."""
+    for seed, new, old, r in ((400, [1, 1], [700, 5], 100), (401, [1], [3000], FULL), (402, [400], [9], 40)):
+        s = Step(seed, F16, bits, new, old, 4, 2, 128, 32, r).to_gpu()
+        out = torch.full((s.N, 4, 132 + shift % 4), 3.0, dtype=F16, device="cuda")
+        got = kv_cache.fwd(s.cache, s.plan, s.q.cuda(), out=out[..., shift:shift + 128])
+        s.check(got)
+        assert (out[..., :shift] == 3).all() and (out[..., shift + 128:] == 3).all()
