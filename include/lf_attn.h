@@ -250,8 +250,10 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  *            (scale, mid).  With n = d / 32, a K row is 32-bit words [4][n],
  *            word [c][g] holding values 32 g + 8 c + 0..7 from its lowest
  *            four bits up; a V row is 16-bit units [8][n], unit [r][g]
- *            holding values 32 g + 4 r + 0..3.  Values are in fp16's range:
- *            the attention reads a V value as the nearest fp16.
+ *            holding values 32 g + 4 r + 0..3.  Values are under 2^17 - 64
+ *            in magnitude (an appended group's are, its rounded parameters may
+ *            take them to 65568); the attention reads a V value rounded to
+ *            fp16's 11 bits.
  * dtype is LF_BF16 or LF_F16 (queries, output, dense rows), d is 64 or 128,
  * q_heads <= 128 a multiple of kv_heads, n_pages * kv_heads * page < 2^31,
  * max_pages * page <= 2^30.  Cache and par pointers are 16-byte aligned.

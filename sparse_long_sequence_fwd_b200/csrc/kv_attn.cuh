@@ -42,9 +42,10 @@
 // fp32 sum (what that loses is 1024 steps of 2^-24 of the q sum).  Queries are
 // brought to [-2, 2] by a power of two for it, which f16 holds exactly down to
 // 2^-14 of the largest, and to 2^-25 of it below.  V is made f16 values, one
-// rounding (2^-11).  Bound here: instructions, about 28 a key and warp at d =
+// rounding (2^-11); those past its range are halved first and weigh twice
+// (double_large).  Bound here: instructions, about 28 a key and warp at d =
 // 128, half of them integer ones to spread nibbles (4 sequences of 32768 to
-// 65536 tokens, 8 kv heads of 128: 264 MB in 77 us, 52 % of the copy rate).
+// 65536 tokens, 8 kv heads of 128: 264 MB in 79 us, 51 % of the copy rate).
 //
 // Rounding: scores, maxima, sums and O in fp32.  P goes to the tensor cores in
 // two bf16 (2^-15) or f16 parts (2^-20): the second part's MMAs are free where
@@ -304,8 +305,9 @@ struct KvState {
     static constexpr bool kSplitP = kBits == 4 && kHalf;
     // P = 2^(score - base + kLift), at most 2^(kLift + kRoom).  An f16 P is lifted so that a weight 2^-36 of the
     // largest still counts: a million such keys are 2^-16 of the sum.
+    // (Over 4 bits one power of two is left free for double_large.)
     static constexpr bool kHalfP = kBits == 4 || kHalf;
-    static constexpr float kLift = kHalfP ? 11.f : 0.f, kRoom = kHalfP ? 4.f : 8.f;
+    static constexpr float kLift = kHalfP ? 11.f : 0.f, kRoom = kBits == 4 ? 3.f : kHalf ? 4.f : 8.f;
     uint32_t q[kNt][HD / 16][2];
     float o[kNt][HD / 16][4];
     float m[kNt][2], l[kNt][2];  // (o[.][4 j + t][i]: dimension 64 j + 8 g + 2 t + (i >> 1); 4 bits: [2 j + t]: 32 j + 4 g + ..)
@@ -547,6 +549,42 @@ struct KvState {
         }
     }
 
+    // mid + scale (c - 8) may be past the largest fp16 though the group's values are not (up to 65568: both parameters and the
+    // code are rounded).  Such keys have their V parameters halved in the stage and their weights doubled.
+    // large_values: whether this lane's key of the stage may be one; what is left alone is under 49152 + 8 * 2048 in magnitude.
+    // (One read, four comparisons and a share of the vote on the base: 76.3 -> 79.1 us at 4 sequences of up to 65536 tokens,
+    // 14.1 -> 14.4 at 64 windows.  Clamping each value instead takes two instructions for every two of them.)
+    static __device__ __forceinline__ uint8_t* v_params(uint8_t* stage, int lane) {
+        using St = KvStage<HD, kBits>;
+        return stage + (lane >> 4) * St::kSubBytes + St::kVp + (lane & 15) * St::kPar;
+    }
+    static __device__ __forceinline__ bool large_values(uint8_t* stage, int lane) {
+        uint32_t w[kGroups];  // (scale, mid)
+        load_words(w, v_params(stage, lane));
+        const __half2* par = reinterpret_cast<const __half2*>(w);
+        __half2 top = __hmax2(__habs2(par[0]), __habs2(par[1]));
+        if constexpr (kGroups == 4) top = __hmax2(top, __hmax2(__habs2(par[2]), __habs2(par[3])));
+        return !__hbltu2(top, __floats2half2_rn(2048.f, 49152.f));  // (a group that is NaN need not be one)
+    }
+    // (Halved, a subnormal parameter of another group of such a key is off by 2^-25.)
+    static __device__ __forceinline__ void double_large(float (&s)[KvStage<HD, kBits>::kSub][kNt][4], uint8_t* stage,
+                                                        int lane, uint32_t keys) {
+        if ((keys >> lane) & 1) {
+            __half2* par = reinterpret_cast<__half2*>(v_params(stage, lane));
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) par[j] = __hmul2(par[j], __float2half2_rn(0.5f));
+        }
+        __syncwarp();
+        const int g = lane >> 2;
+#pragma unroll
+        for (int u = 0; u < KvStage<HD, kBits>::kSub; ++u)
+#pragma unroll
+            for (int n = 0; n < kNt; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((keys >> (16 * u + 8 * (i >> 1) + g)) & 1) s[u][n][i] *= 2.f;
+    }
+
     // The A operands of value tile T (two dimensions of this lane): keys 2c, 2c + 1 beside each other, then 2c + 8, 2c + 9.
     static __device__ __forceinline__ void value_tile(const KvRegs<HD, kBits>& x, int T, uint32_t (&a)[4]) {
         if constexpr (kBits == 16) {
@@ -654,11 +692,13 @@ struct KvState {
 
     // One step over a stage; bit i of ok: there is a key i.  masked (kPack): not every row sees every key.
     template <typename Tile>
-    __device__ __forceinline__ void step(const uint8_t* stage, int g, int c, uint32_t ok, bool masked, int code,
+    __device__ __forceinline__ void step(uint8_t* stage, int g, int c, uint32_t ok, bool masked, int code,
                                          const Tile& tile) {
         constexpr int kSub = KvStage<HD, kBits>::kSub;
         constexpr uint32_t kAll = kSub == 2 ? ~0u : 0xffffu;
         float s[kSub][kNt][4];
+        bool large = false;
+        if constexpr (kBits == 4) large = large_values(stage, 4 * g + c);
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
             scores(s[u], stage + u * KvStage<HD, kBits>::kSubBytes, g, c);
@@ -698,7 +738,8 @@ struct KvState {
         // The exponent base moves only when a score exceeds it by more than
         // kRoom (or there is none yet).
         float top[kNt][2];
-        bool move = false;
+        bool move = large;
+        uint32_t keys = 0;  // 4 bits: those of large values
 #pragma unroll
         for (int n = 0; n < kNt; ++n)
 #pragma unroll
@@ -708,6 +749,7 @@ struct KvState {
                 move |= top[n][e] > m[n][e] + kRoom;
             }
         if (__any_sync(~0u, move)) {
+            if constexpr (kBits == 4) keys = __ballot_sync(~0u, large);
 #pragma unroll
             for (int n = 0; n < kNt; ++n)
 #pragma unroll
@@ -739,6 +781,8 @@ struct KvState {
                         l[n][e] += s[u][n][i];
                     }
             }
+        if constexpr (kBits == 4)
+            if (keys) double_large(s, stage, 4 * g + c, keys);
         if constexpr (kPack)
             if (masked) {
 #pragma unroll
