@@ -283,7 +283,8 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  *   k, v        DEVICE rows [n_tokens][kv_heads][d]; q [n_tokens][q_heads][d]
  *               or NULL: queries to turn into q_out
  *   k_held, v_held   DEVICE dense rows for what the cache now holds (the
- *               dequantised values for bits 4), or NULL
+ *               dequantised values for bits 4, in f16 those past its range as
+ *               +-65504), or NULL
  *   strides     HOST int64 [12]: (token, head) strides in elements of k, v,
  *               q, k_held, v_held, q_out (those of NULL rows are not read),
  *               below 2^31; no output may overlap an input

@@ -126,6 +126,27 @@ __device__ __forceinline__ void quantise8(uint4 raw, bool is_k, bool on, int cc,
             uint32_t(__half_as_ushort(hs)) | uint32_t(__half_as_ushort(hm)) << 16;
 }
 
+// Eight values that the cache now holds to a dense row.  f16: those past its range (up to 65568, where the group's ends
+// are +-65504) as the nearest finite one; NaN stays NaN.
+template <typename T>
+__device__ __forceinline__ void store_held(T* y, const float (&x)[8], bool wide) {
+    if constexpr (std::is_same<T, __half>::value) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("cvt.rn.satfinite.f16x2.f32 %0, %2, %1;" : "=r"(w[i]) : "f"(x[2 * i]), "f"(x[2 * i + 1]));
+        if (wide) *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = __ushort_as_half(static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1))));
+    } else {
+        if (wide) RowIo<T>::store8(y, x);
+        else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) RowIo<T>::store(y + i, x[i]);
+    }
+}
+
 // kW as in rotary_kernel.  grid: (tiles of tokens, 1 or 3): with 3 a CTA takes k, v or q only, where
 // tiles alone are too few to fill the GPU.  smem: (cos, sin) [tile][cs_stride]; 4 bits: the
 // turned k and v rows [k heads + v heads][tile][d] in 16 bits.
@@ -267,10 +288,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) kv_append_kernel(const 
                     T* y = static_cast<T*>(p.y[w]) + int64_t(n0 + a) * p.yt[w] + int64_t(h) * p.yh[w] + 8 * ch;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) c8[k] = fmaf(scale, c8[k], mid);
-                    if (p.wide) RowIo<T>::store8(y, c8);
-                    else
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) RowIo<T>::store(y + k, c8[k]);
+                    store_held<T>(y, c8, p.wide);
                 }
             }
         }

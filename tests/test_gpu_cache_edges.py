@@ -32,3 +32,29 @@ def test_4_bit_values_past_the_largest_fp16(form, dtype, d):
     assert 65520 <= rows.max() < 2 * 65504
     s.to_gpu()
     s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_4_bit_groups_at_the_ends_of_fp16_are_held_finite(dtype):
+    """Rows appended with both ends of fp16 in a group: codes and parameters by the formula, held rows the nearest finite
+    values, the attention of a token over them finite."""
+    s = Step(510, dtype, 4, [40], [0], 2, 2, 64, 16, FULL)
+    g = gen(2)
+    v = (40000 * torch.randn(40, 2, 64, generator=g)).clamp(-65000, 65000)
+    v[..., 3], v[..., 40] = 65504.0, -65504.0
+    v[::2, :, 7], v[1::2, :, 50] = -65504.0, 65504.0
+    if dtype == BF16:
+        v = v.clamp(-65280, 65280)
+    s.v = v.to(dtype)
+    s.to_gpu()
+    _, _, hv = kv_cache.append(s.cache, s.plan, s.k.cuda(), s.v.cuda(), held=True)
+    codes, par = ref.quantise(s.v)
+    want = (par[..., 1:].double() + par[..., :1].double() * (codes.double() - 8).unflatten(-1, (2, 32))).flatten(-2)
+    top = torch.finfo(dtype).max
+    assert want.abs().max() > 65504 or dtype == BF16
+    assert torch.equal(hv.cpu(), want.clamp(-top, top).to(dtype))
+    s.cpu = [t.cpu() for t in (s.cache.k, s.cache.v, s.cache.k_par, s.cache.v_par)]
+    s.context[:], s.cu, s.N, s.rows = 39, torch.tensor([0, 1], dtype=torch.int32), 1, [(0, 39)]
+    s.q = s.q[:1]
+    s.to_gpu()
+    s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
