@@ -304,10 +304,9 @@ struct KvState {
     static constexpr int kGroups = HD / 32;
     static constexpr bool kSplitP = kBits == 4 && kHalf;
     // P = 2^(score - base + kLift), at most 2^(kLift + kRoom).  An f16 P is lifted so that a weight 2^-36 of the
-    // largest still counts: a million such keys are 2^-16 of the sum.
-    // (Over 4 bits one power of two is left free for double_large.)
-    static constexpr bool kHalfP = kBits == 4 || kHalf;
-    static constexpr float kLift = kHalfP ? 11.f : 0.f, kRoom = kBits == 4 ? 3.f : kHalf ? 4.f : 8.f;
+    // largest still counts (2^-37 over 16 bits): a million such keys are 2^-16 of the sum.  Over 4 bits one power of two is
+    // left free for double_large; over 16 bits it goes into the lift, since no weight is under 2^-23 (values()).
+    static constexpr float kLift = kBits == 4 ? 11.f : kHalf ? 12.f : 0.f, kRoom = kBits == 4 || kHalf ? 3.f : 8.f;
     uint32_t q[kNt][HD / 16][2];
     float o[kNt][HD / 16][4];
     float m[kNt][2], l[kNt][2];  // (o[.][4 j + t][i]: dimension 64 j + 8 g + 2 t + (i >> 1); 4 bits: [2 j + t]: 32 j + 4 g + ..)
@@ -473,14 +472,17 @@ struct KvState {
             for (int n = 0; n < kNt; ++n) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    // toward 0, and what that leaves: never 0 or less, so that it times an infinite value is one
-                    const float p0 = s[n][2 * i], p1 = s[n][2 * i + 1];
+                    // Toward 0, and what that leaves.  Neither part is 0, so that infinite values under any weight are
+                    // infinities: f16 parts are 2^-24 at least, 2^-35 of the largest weight together, bf16 ones are not 0 where
+                    // the fp32 weight is not (2^-126 of the largest).
                     if constexpr (kHalf) {
+                        const float p0 = fmaxf(s[n][2 * i], 0x1p-24f), p1 = fmaxf(s[n][2 * i + 1], 0x1p-24f);
                         const uint32_t hi = pack_f16x2_rz(p0, p1);
                         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
                         b[n][i] = movmatrix_t(hi);
                         b2[n][i] = movmatrix_t(pack_f16x2(fmaxf(p0 - f.x, 0x1p-24f), fmaxf(p1 - f.y, 0x1p-24f)));
                     } else {
+                        const float p0 = s[n][2 * i], p1 = s[n][2 * i + 1];
                         const uint32_t u = __float_as_uint(p0), w = __float_as_uint(p1);
                         b[n][i] = movmatrix_t(__byte_perm(u, w, 0x7632));
                         b2[n][i] = movmatrix_t(pack_bf16x2(fmaxf(p0 - __uint_as_float(u & 0xffff0000u), 1e-37f),
@@ -624,7 +626,11 @@ struct KvState {
         for (int n = 0; n < kNt; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float p0 = s[n][2 * i], p1 = s[n][2 * i + 1];
+                float p0 = s[n][2 * i], p1 = s[n][2 * i + 1];
+                if constexpr (kHalf && kBits == 16) {
+                    if (p0 != 0.f) p0 = fmaxf(p0, 0x1p-24f);
+                    if (p1 != 0.f) p1 = fmaxf(p1, 0x1p-24f);
+                }
                 uint32_t hi;
                 float2 f;
                 if constexpr (kF16) {

@@ -1,4 +1,6 @@
 """The paged cache at the ends of its types and shapes, against the definitions in 64 bits."""
+import math
+
 import pytest
 import torch
 
@@ -58,3 +60,34 @@ def test_4_bit_groups_at_the_ends_of_fp16_are_held_finite(dtype):
     s.q = s.q[:1]
     s.to_gpu()
     s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
+
+
+@pytest.mark.parametrize("dtype,d", [(F16, 64), (BF16, 64), (F16, 128)])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_infinite_values_under_small_weights(form, dtype, d):
+    """A value of +-infinity under e^-22 (2^-32), e^-40 and e^-60 of the largest weight is an infinity in the rows that see
+    it, in that dimension alone, and nothing elsewhere."""
+    new, old, hq, hkv, r = FORMS[form]
+    s = Step(520 + d, dtype, 16, new, old, hq, hkv, d, 16, r)
+    s.q.zero_()
+    s.q[..., 0] = 8.0
+    s.cpu[0][..., 0] = 10.0
+    p0 = max(0, old[0] - 30)
+    for i, (down, x) in enumerate(((22, math.inf), (40, -math.inf), (60, math.inf))):
+        at = int(s.table[0, (p0 + i) // 16]), slice(None), (p0 + i) % 16
+        s.cpu[0][at][..., 0] = 10.0 - down / 8.0
+        s.cpu[1][at][..., 5 + i] = x
+    s.to_gpu()
+    got = kv_cache.fwd(s.cache, s.plan, s.q.cuda(), scale=1.0).double().cpu()
+    other = [e for e in range(d) if e not in (5, 6, 7)]
+    seen = 0
+    for n, (b, p) in enumerate(s.rows):
+        keys = ref.key_set(p, r, 1, None)
+        for i, x in enumerate((math.inf, -math.inf, math.inf)):
+            if b == 0 and p0 + i in keys and p - p0 > 2 and max(keys) > p0 + 2:
+                assert (got[n, :, 5 + i] == x).all(), (n, b, p, i, got[n, :, 5 + i])
+                seen += 1
+            elif b == 1 or p0 + i not in keys:
+                assert torch.isfinite(got[n, :, 5 + i]).all(), (n, b, p, i)
+        assert torch.isfinite(got[n][:, other]).all(), (n, b, p)
+    assert seen >= 3
