@@ -40,8 +40,9 @@
 // up), so all MMAs are f16 here.  K stays codes: q . k = sum over groups of
 // scale (sum of q (c - 8)) + mid (sum of q) in fp32, the 1024 taken off the
 // fp32 sum (what that loses is 1024 steps of 2^-24 of the q sum).  Queries are
-// brought to [-2, 2] by a power of two for it, which f16 holds exactly down to
-// 2^-14 of the largest, and to 2^-25 of it below.  V is made f16 values, one
+// brought to +-2^14 by a power of two for it, and every second one, whose codes
+// are 16 times theirs, to 2^10: f16 holds them exactly down to 2^-23 of the
+// largest, and to 2^-34 of it below.  V is made f16 values, one
 // rounding (2^-11); those past its range are halved first and weigh twice
 // (double_large).  Bound here: instructions, about 28 a key and warp at d =
 // 128, half of them integer ones to spread nibbles (4 sequences of 32768 to
@@ -348,7 +349,7 @@ struct KvState {
                 }
                 rs[n][0] = rs[n][1] = sl2;
             } else {
-                // query head g of the tile: its largest |q|, and the power of two that brings it to [1, 2)
+                // query head g of the tile: its largest |q|, and the power of two that brings it to [2^13, 2^14)
                 float f[HD / 32][8], top = 0.f;
 #pragma unroll
                 for (int j = 0; j < HD / 32; ++j) {
@@ -365,9 +366,9 @@ struct KvState {
                 }
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                const uint32_t x8 = __float_as_uint(top) >> 23, e = x8 == 254 ? 253 : x8;  // 255: an infinity: no scaling
-                const float down = e == 255 ? 1.f : __uint_as_float((254u - e) << 23);
-                const float up = e == 255 ? 1.f : __uint_as_float(e << 23);
+                const uint32_t e = max(__float_as_uint(top) >> 23, 14u);  // 255: an infinity: no scaling; under 2^-113: as that
+                const float down = e == 255 ? 1.f : __uint_as_float((267u - e) << 23);
+                const float up = e == 255 ? 1.f : __uint_as_float((e - 13u) << 23);
                 rs[n][0] = sl2 * __shfl_sync(~0u, up, 8 * c);
                 rs[n][1] = sl2 * __shfl_sync(~0u, up, 8 * c + 4);
 #pragma unroll

@@ -91,3 +91,32 @@ def test_infinite_values_under_small_weights(form, dtype, d):
                 assert torch.isfinite(got[n, :, 5 + i]).all(), (n, b, p, i)
         assert torch.isfinite(got[n][:, other]).all(), (n, b, p)
     assert seen >= 3
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,hq", [(64, 1), (128, 1), (64, 12), (128, 4)])
+def test_small_4_bit_queries_beside_a_large_one(d, hq, dtype):
+    """One query value of 1 and, in the other groups, values of 2^-11 (1 + 2^-10) (2^-11 (1 + 2^-7) in bf16) at odd and even
+    places: every other key has +7 under the odd and -7 under the even ones, so that its score is 0 as the others' are."""
+    x = 2.0 ** -11 * (1 + (2.0 ** -10 if dtype == F16 else 2.0 ** -7))
+    s = Step(530, dtype, 4, [1], [255], hq, 1, d, 16, FULL, pages_more=0)
+    s.q.zero_()
+    s.q[..., 0] = 1.0
+    s.q[..., 32:] = x
+    codes = torch.full((s.cpu[0].shape[0], 1, 16, d), 8)
+    codes[:, :, ::2, 32::2], codes[:, :, ::2, 33::2] = 1, 15
+    s.cpu[0] = ref.pack(codes, True)
+    s.cpu[2][..., 0], s.cpu[2][..., 1] = 1.0, 0.0
+    codes[:, :, ::2], codes[:, :, 1::2] = 15, 0  # values 1.75 and -2: a weight that moves shows
+    s.cpu[1], s.cpu[3][..., 0], s.cpu[3][..., 1] = ref.pack(codes, False), 0.25, 0.0
+    s.to_gpu()
+    scale = 1000.0
+    got = kv_cache.fwd(s.cache, s.plan, s.q.cuda(), scale=scale).double().cpu()
+    want, by, _ = ref.attend(s.q, s.cpu, s.table, s.rows, s.r, s.dil, None, scale)
+    # fp32: a group's sum of q (1024 + c), c < 16, four accumulations that may truncate (2^-23 each) and one rounding when the
+    # 1024 is taken off; two such at most move a weight by that share, and its base's share the sum
+    score = scale * 5 * 2.0 ** -23 * 1040 * (d - 32) * x
+    u = torch.finfo(dtype).eps / 2
+    tol = (2.0 ** -10 + 2.0 ** -12) * by + u * want.abs() + score * (by + want.abs())
+    assert score < 0.04
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
