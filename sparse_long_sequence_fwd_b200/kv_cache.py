@@ -23,6 +23,7 @@ from .rotary import _check_freqs, _on_stream
 
 _PACK4, _PACK12 = struct.Struct("4q").pack, struct.Struct("12q").pack
 _CODES = {torch.bfloat16: LF_BF16, torch.float16: LF_F16}
+_MOST = (1 << 31) - 1
 
 
 def _int32(t: torch.Tensor, shape, what: str) -> torch.Tensor:
@@ -88,8 +89,18 @@ class Plan:
             raise ValueError("context must be [n_seqs] and table [n_seqs, max_pages]")
         S = context.shape[0]
         self.n_seqs, self.n_tokens, self.q_heads, self.kv_heads = S, int(n_tokens), int(q_heads), cache.kv_heads
+        if not 0 <= self.n_tokens <= _MOST or not 1 <= self.q_heads <= _MOST:
+            raise ValueError("n_tokens must not be negative and q_heads at least 1, both in 32 bits")
         self.page, self.max_pages = cache.page, table.shape[1]
-        self.r = (1 << 31) - 1 if r is None else int(r)
+        # the library's sizes have 32 bits; past them a window is all of a sequence, and a dilation past its length
+        self.r = _MOST if r is None else min(int(r), _MOST)
+        if self.r < 0:
+            raise ValueError("r must not be negative")
+        if dil is not None:
+            dil = [dil] * cache.kv_heads if isinstance(dil, int) else [int(x) for x in dil]
+            if min(dil, default=1) < 1:
+                raise ValueError("dil must be at least 1")
+            dil = [min(x, _MOST) for x in dil]
         self.dil = _dil_array(dil, cache.kv_heads)
         self.table = _int32(table, (S, self.max_pages), "table")
         self.cu_tokens = _int32(cu_tokens, (S + 1,), "cu_tokens")

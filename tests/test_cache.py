@@ -188,3 +188,15 @@ def test_the_packing_is_one_to_one():
             c = torch.randint(0, 16, (5, d), generator=torch.Generator().manual_seed(d))
             assert sorted(ref.place(d, is_k).tolist()) == list(range(d))
             assert torch.equal(ref.unpack(ref.pack(c, is_k), is_k), c)
+
+
+def test_sizes_past_32_bits_do_not_wrap():
+    cache = kv_cache.KVCache(torch.zeros(4, 2, 8, 64).half(), torch.zeros(4, 2, 8, 64).half())
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    for kw in (dict(r=-1), dict(r=-(1 << 32) + 5), dict(r=3, dil=0), dict(r=3, dil=[1, 1 - (1 << 32)])):
+        with pytest.raises(ValueError, match="r must|dil must"):
+            kv_cache.Plan(cache, i(2, 3), i(3), i(2), 2, 4, **kw)
+    for kw in (dict(n_tokens=(1 << 32) + 2, q_heads=4), dict(n_tokens=2, q_heads=(1 << 32) + 4), dict(n_tokens=-1, q_heads=4),
+               dict(n_tokens=2, q_heads=0)):
+        with pytest.raises(ValueError, match="n_tokens|q_heads"):
+            kv_cache.Plan(cache, i(2, 3), i(3), i(2), r=3, **kw)

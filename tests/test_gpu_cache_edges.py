@@ -120,3 +120,16 @@ def test_small_4_bit_queries_beside_a_large_one(d, hq, dtype):
     tol = (2.0 ** -10 + 2.0 ** -12) * by + u * want.abs() + score * (by + want.abs())
     assert score < 0.04
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
+
+
+def test_windows_and_dilations_past_32_bits():
+    s = Step(560, BF16, 16, [1], [300], 2, 2, 64, 16, FULL).to_gpu()
+    q = s.q.cuda()
+    plan = lambda r, dil=None: kv_cache.Plan(  # noqa: E731
+        s.cache, s.table.cuda(), s.cu.cuda(), s.context.cuda(), 1, 2, r, dil=dil)
+    want = kv_cache.fwd(s.cache, s.plan, q)
+    for r in (None, (1 << 31) - 1, 1 << 31, 1 << 32, (1 << 32) + 3, 1 << 70):
+        assert torch.equal(kv_cache.fwd(s.cache, plan(r), q), want), r
+    s.dil = [1 << 20] * 2  # the token's own key alone
+    for dil in (1 << 20, (1 << 31) - 1, 1 << 31, (1 << 32) + 1):
+        s.check(kv_cache.fwd(s.cache, plan(7, dil), q))
