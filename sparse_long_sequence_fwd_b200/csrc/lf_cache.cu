@@ -40,6 +40,15 @@ struct Span {
     bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
 };
 
+// The strides that are stepped by: nothing steps along a dimension of one, whatever its stride.
+template <int kDims>
+struct Strides {
+    int64_t s[kDims];
+    Strides(const int64_t* n, const int64_t* given) {
+        for (int i = 0; i < kDims; ++i) s[i] = n[i] > 1 ? given[i] : 0;
+    }
+};
+
 // Sizes n[i] with strides s[i] (elements) and d contiguous values behind.
 // False: a negative stride, or a place past 2^46 bytes.
 bool span_of(const void* p, int dims, const int64_t* n, const int64_t* s, int d, size_t es, Span* out) {
@@ -300,8 +309,8 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
         if (!x[a]) continue;
         if (!aligned(x[a], ei) || !aligned(y[a], eo)) return LF_ERR_INVALID_ARG;
         const int64_t n[3] = {B, p.heads[a], T};
-        const int64_t* xs = strides + 3 * a;
-        const int64_t* ys = strides + 9 + 3 * a;
+        const Strides<3> by_x(n, strides + 3 * a), by_y(n, strides + 9 + 3 * a);
+        const int64_t *xs = by_x.s, *ys = by_y.s;
         if (!span_of(x[a], 3, n, xs, d, ei, &in[a]) || !span_of(y[a], 3, n, ys, d, eo, &out[a]) || !distinct(3, n, ys))
             return LF_ERR_INVALID_ARG;
         wide = wide && by_eight(x[a], 3, xs, ei) && by_eight(y[a], 3, ys, eo);
@@ -396,8 +405,8 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     for (int a = 0; a < 3; ++a) {
         p.heads[a] = a < 2 ? kv_heads : (q ? q_heads : 0);
         const int64_t n[2] = {n_tokens, p.heads[a]};
-        const int64_t* xs = strides + 2 * a;
-        const int64_t* ys = strides + 6 + 2 * a;
+        const Strides<2> by_x(n, strides + 2 * a), by_y(n, strides + 6 + 2 * a);
+        const int64_t *xs = by_x.s, *ys = by_y.s;
         if (x[a]) {
             if (!aligned(x[a], 2) || !span_of(x[a], 2, n, xs, d, 2, &in[a])) return LF_ERR_INVALID_ARG;
             if (!small(xs)) return LF_ERR_UNSUPPORTED;
@@ -481,9 +490,10 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     if (st != LF_OK) return st;
     if ((st = check_cache(k_cache, v_cache, k_par, v_par, n_pages, kv_heads, page, dtype, bits)) != LF_OK) return st;
     const int64_t n[2] = {n_tokens, q_heads};
+    const Strides<2> by_q(n, strides), by_out(n, strides + 2);
     Span a, b;
-    if (!span_of(q, 2, n, strides, d, 2, &a) || !span_of(out, 2, n, strides + 2, d, 2, &b) ||
-        !distinct(2, n, strides + 2) || !by_eight(q, 2, strides, 2) || !aligned(out, 2) || a.meets(b))
+    if (!span_of(q, 2, n, by_q.s, d, 2, &a) || !span_of(out, 2, n, by_out.s, d, 2, &b) ||
+        !distinct(2, n, by_out.s) || !by_eight(q, 2, by_q.s, 2) || !aligned(out, 2) || a.meets(b))
         return LF_ERR_INVALID_ARG;
     const uint64_t need = workspace_of(sh, d, bits);
     if (need > 0 && !workspace) return LF_ERR_INVALID_ARG;
@@ -496,11 +506,11 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     if ((st = device_info(s, &p.status, &sms)) != LF_OK || (st = kernel_limits()) != LF_OK) return st;
     p.q = q;
     p.out = out;
-    p.q_row = strides[0];
-    p.q_head = strides[1];
-    p.o_wide = aligned(out, 8) && strides[2] % 4 == 0 && strides[3] % 4 == 0;
-    p.o_row = strides[2];
-    p.o_head = strides[3];
+    p.q_row = by_q.s[0];
+    p.q_head = by_q.s[1];
+    p.o_wide = aligned(out, 8) && by_out.s[0] % 4 == 0 && by_out.s[1] % 4 == 0;
+    p.o_row = by_out.s[0];
+    p.o_head = by_out.s[1];
     p.k = static_cast<const uint8_t*>(k_cache);
     p.v = static_cast<const uint8_t*>(v_cache);
     p.k_par = static_cast<const uint8_t*>(k_par);

@@ -4,9 +4,9 @@ import math
 import pytest
 import torch
 
-from sparse_long_sequence_fwd_b200 import kv_cache
+from sparse_long_sequence_fwd_b200 import kv_cache, rotary
 from tests import cache_ref as ref
-from tests.test_gpu_cache import BF16, F16, FULL, Step, _lib, _no_flags, gen  # noqa: F401
+from tests.test_gpu_cache import BF16, F16, FULL, Step, _lib, _no_flags, gen, turn_tolerance  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +133,26 @@ def test_windows_and_dilations_past_32_bits():
     s.dil = [1 << 20] * 2  # the token's own key alone
     for dil in (1 << 20, (1 << 31) - 1, 1 << 31, (1 << 32) + 1):
         s.check(kv_cache.fwd(s.cache, plan(7, dil), q))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_strides_of_dimensions_of_one(dtype):
+    """One token of a packed row that is no multiple of 16 bytes, and heads of one: strides that nothing steps by."""
+    s = Step(570, dtype, 16, [1], [70], 4, 1, 64, 16, 40).to_gpu()
+    wide = torch.zeros(2, 6 * 64 + 1, dtype=dtype)
+    wide[0, :256], wide[0, 256:320], wide[0, 320:384] = s.q.flatten(), s.k.flatten(), s.v.flatten()
+    wide = wide.cuda()
+    q, k, v = (torch.as_strided(wide, (1, h, 64), (385, 64, 1), 64 * a) for h, a in ((4, 0), (1, 4), (1, 5)))
+    s.check(kv_cache.fwd(s.cache, s.plan, q))
+    f = rotary.freqs(64, device="cuda")
+    got = kv_cache.append(s.cache, s.plan, k, v, q=q, freqs=f)
+    want = ref.turn(s.q.double(), torch.tensor([70])[:, None], f.tolist())
+    assert ((got.double().cpu() - want).abs() <= turn_tolerance(s.q.double(), want, dtype, 1.0)).all()
+    far = torch.as_strided(wide, (1, 1, 64), (1 << 40, 1 << 41, 1))
+    other = Step(571, dtype, 16, [1], [70], 1, 1, 64, 16, 40).to_gpu()
+    other.q = far.cpu()
+    other.check(kv_cache.fwd(other.cache, other.plan, far))
+    one = torch.as_strided(wide, (1, 1, 1, 64), (1 << 41, 1 << 40, 1 << 39, 1))
+    got = rotary.fwd(one, freqs=f, pos=torch.tensor([9], dtype=torch.int32, device="cuda"))[0]
+    want = ref.turn(one.double().cpu(), torch.tensor([9]), f.tolist())
+    assert ((got.double().cpu() - want).abs() <= turn_tolerance(one.double().cpu(), want, dtype, 1.0)).all()
