@@ -267,7 +267,8 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  *   cu_tokens   DEVICE int32 [n_seqs + 1], from 0 and not decreasing: rows
  *               [cu[s], cu[s+1]) of the step's n_tokens token rows are
  *               sequence s's new tokens.  Rows from cu[n_seqs] on are no
- *               tokens: every call leaves their outputs as they were.
+ *               tokens: every call leaves their outputs as they were.  Where
+ *               cu decreases no row is one (flagged).
  *   context     DEVICE int32 [n_seqs]: tokens of the sequence before these,
  *               so row cu[s] + i is at position context[s] + i
  *   global_idx  DEVICE int32 [n_seqs, n_global], any order, duplicates

@@ -180,13 +180,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
     __shared__ int64_t s_prefix[kPlanRows], s_bound[kKvMaxCtas + 1], s_warp[32], s_carry;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s_carry = 0;
+    bool falls = false;
     for (int s = tid; s <= sh.S; s += kPlanThreads) {
         const int c = cu[s];
         if (s <= kPlanSeqs) s_cu[s] = c;
+        falls |= s > 0 && c < cu[s - 1];
         if (s == 0 ? c != 0 : c < cu[s - 1]) atomicOr(status, kStatusBadCache);
         if (s == sh.S && c > sh.N) atomicOr(status, kStatusBadCache);
     }
-    __syncthreads();
+    const bool none = __syncthreads_or(falls);  // else two sequences, and two tiles, could have one row
     const int32_t* cus = sh.S <= kPlanSeqs ? s_cu : cu;
     const int64_t* prefix = sh.N <= kPlanRows ? s_prefix : p.prefix;
     const int unit_cost = kUnitKeys / sh.block;
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_rows_kernel(const int32_
             }
             const int c0 = cus[lo], c1 = cus[lo + 1];
             int seq = -1, pos = 0, ng = 0;
-            if (c0 >= 0 && c0 <= n && n < c1) {
+            if (!none && c0 >= 0 && c0 <= n && n < c1) {
                 const int before = context[lo];
                 const int64_t at = int64_t(before) + (n - c0);
                 if (before >= 0 && at < sh.max_len) {

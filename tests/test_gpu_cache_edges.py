@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from sparse_long_sequence_fwd_b200 import kv_cache, rotary
+from sparse_long_sequence_fwd_b200 import kv_cache, lf_attn, rotary
 from tests import cache_ref as ref
 from tests.test_gpu_cache import BF16, F16, FULL, Step, _lib, _no_flags, gen, turn_tolerance  # noqa: F401
 
@@ -120,6 +120,25 @@ def test_small_4_bit_queries_beside_a_large_one(d, hq, dtype):
     tol = (2.0 ** -10 + 2.0 ** -12) * by + u * want.abs() + score * (by + want.abs())
     assert score < 0.04
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
+
+
+@pytest.mark.parametrize("cu", [[0, 430, 10, 530, 250], [0, 350, 260, 290, 120], [0, 700, 0, 700, 700]])
+def test_no_row_is_one_where_cu_tokens_decreases(cu):
+    """Rows that two sequences could claim: none is taken, in tiles or single rows, by the cache or the attention; flagged."""
+    for dil in (1, 2):
+        s = Step(555, BF16, 16, [200, 300, 150, 50], [10, 0, 40, 3], 2, 2, 64, 16, 30, dil=dil)
+        s.cu = torch.tensor(cu, dtype=torch.int32)
+        s.to_gpu()
+        before = s.cache.k.clone(), s.cache.v.clone()
+        q, out = s.q.cuda(), torch.full((700, 2, 64), 2.0, dtype=BF16, device="cuda")
+        kv_cache.append(s.cache, s.plan, s.k.cuda(), s.v.cuda())
+        kv_cache.fwd(s.cache, s.plan, q, out=out)
+        assert (out == 2).all()
+        assert torch.equal(s.cache.k, before[0]) and torch.equal(s.cache.v, before[1])
+        assert lf_attn.device_status() == (5, 4)
+        s.plan.cu_tokens.copy_(torch.tensor([0, 200, 500, 650, 700]))
+        s.plan.refresh()
+        s.check(kv_cache.fwd(s.cache, s.plan, q))
 
 
 def test_windows_and_dilations_past_32_bits():
