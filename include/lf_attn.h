@@ -208,9 +208,10 @@ lf_status lf_attn_merge_rows(const float* ml, const float* acc, int n_parts, int
  *               together with its output, not all three
  *   strides     HOST int64 [18]: (sample, head, token) strides in elements of
  *               q, k, v, q_out, k_out, v_out; the d values of a row are
- *               contiguous.  Strides of inputs may be 0, those of outputs
- *               not; no output may overlap an input.  Head and token strides
- *               are below 2^31.
+ *               contiguous.  Strides of inputs may be 0; rows of outputs lie
+ *               apart.  What lies between an output's first and last value
+ *               is no input's.  Head and token strides are below 2^31.  The
+ *               stride of a dimension of one does not count.
  *   B, T, q_heads, kv_heads   sizes; B and T may be 0
  *   d           1..256;  rot: even, 0..d (0: a copy; freqs may be NULL)
  *   pos         DEVICE int32, [T] per sample at a stride of pos_stride (0:
@@ -288,7 +289,7 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  *               +-65504), or NULL
  *   strides     HOST int64 [12]: (token, head) strides in elements of k, v,
  *               q, k_held, v_held, q_out (those of NULL rows are not read),
- *               below 2^31; no output may overlap an input
+ *               below 2^31; outputs as those of lf_attn_rotary
  *   rot == 0    leaves keys and queries as they are
  *   4 bits: scale = fp16((max - min) / 15), mid = fp16(min + 8 scale), c =
  *   (x - mid) / scale + 8 rounded to the nearest, ties to even (8 where scale
@@ -297,10 +298,10 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  *
  * lf_attn_cache_fwd -- the attention of the step's rows over the cache, which
  * already holds their own keys.  q and out: DEVICE rows
- * [n_tokens][q_heads][d], strides HOST int64 [4]: (token, head) of q, of out;
- * q's rows are 16-byte aligned.  Up to 16 / (q_heads / kv_heads) consecutive
- * rows of a sequence (drafts, prompts) share the reading of their keys, unless
- * dil is above 1; a prompt whose window looks both ways belongs to
+ * [n_tokens][q_heads][d], strides HOST int64 [4]: (token, head) of q, of out
+ * (as an output of lf_attn_rotary); q's rows are 16-byte aligned.  Up to
+ * 16 / (q_heads / kv_heads) consecutive rows of a sequence (drafts, prompts)
+ * share the reading of their keys, unless dil is above 1; a prompt whose window looks both ways belongs to
  * lf_attn_fwd.  workspace: DEVICE,
  * lf_attn_cache_workspace_bytes bytes for these sizes (0 where no row's keys
  * are split between CTAs; NULL will do then), 16-byte aligned, of

@@ -65,11 +65,27 @@ bool span_of(const void* p, int dims, const int64_t* n, const int64_t* s, int d,
     return true;
 }
 
-// Rows that are written must not lie on one another: no stride of 0 over more than one.
-bool distinct(int dims, const int64_t* n, const int64_t* s) {
-    for (int i = 0; i < dims; ++i)
-        if (n[i] > 1 && s[i] == 0) return false;
+// Rows that are written must not lie on one another.  False where two that differ along one dimension or two certainly do.
+bool distinct(int dims, const int64_t* n, const int64_t* s, int d) {
+    for (int i = 0; i < dims; ++i) {
+        if (n[i] > 1 && s[i] < d) return false;
+        for (int j = 0; j < i; ++j) {
+            if (n[i] <= 1 || n[j] <= 1) continue;
+            const int a = s[i] >= s[j] ? i : j, b = i + j - a;  // a has the larger stride
+            if (s[a] >= (n[b] - 1) * s[b] + d) continue;
+            for (int64_t k = 1; k < std::min<int64_t>(n[b], 4096); ++k) {  // k steps along b against the nearest along a
+                const int64_t m = k * s[b] / s[a], rest = k * s[b] - m * s[a];
+                if ((m < n[a] && rest < d) || (m + 1 < n[a] && s[a] - rest < d)) return false;
+            }
+        }
+    }
     return true;
+}
+bool same_twice(const void* const* p, int n) {
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < i; ++j)
+            if (p[i] && p[i] == p[j]) return true;
+    return false;
 }
 
 bool by_eight(const void* p, int dims, const int64_t* s, size_t es) {
@@ -302,7 +318,7 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
     const size_t ei = size_of(in_dtype), eo = size_of(out_dtype);
     RotaryParams p{};
     Span in[3], out[3];
-    bool wide = true;
+    bool wide = true, apart_rows = !same_twice(y, 3);
     for (int a = 0; a < 3; ++a) {
         if ((x[a] == nullptr) != (y[a] == nullptr)) return LF_ERR_INVALID_ARG;
         p.heads[a] = x[a] ? (a == 0 ? q_heads : kv_heads) : 0;
@@ -311,8 +327,9 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
         const int64_t n[3] = {B, p.heads[a], T};
         const Strides<3> by_x(n, strides + 3 * a), by_y(n, strides + 9 + 3 * a);
         const int64_t *xs = by_x.s, *ys = by_y.s;
-        if (!span_of(x[a], 3, n, xs, d, ei, &in[a]) || !span_of(y[a], 3, n, ys, d, eo, &out[a]) || !distinct(3, n, ys))
+        if (!span_of(x[a], 3, n, xs, d, ei, &in[a]) || !span_of(y[a], 3, n, ys, d, eo, &out[a]))
             return LF_ERR_INVALID_ARG;
+        apart_rows = apart_rows && distinct(3, n, ys, d);
         wide = wide && by_eight(x[a], 3, xs, ei) && by_eight(y[a], 3, ys, eo);
         p.x[a] = x[a];
         p.y[a] = y[a];
@@ -329,6 +346,7 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
             if (a.meets(b)) return LF_ERR_INVALID_ARG;
     if (in_dtype != out_dtype && in_dtype != LF_F32) return LF_ERR_UNSUPPORTED;
     if (d > kRotMaxD || q_heads > kMaxRotHeads || kv_heads > kMaxRotHeads || B > 65535) return LF_ERR_UNSUPPORTED;
+    if (!apart_rows) return LF_ERR_INVALID_ARG;
     const int heads = p.heads[0] + p.heads[1] + p.heads[2];
     if (B == 0 || T == 0 || heads == 0) return LF_OK;
     p.pos = pos;
@@ -415,7 +433,7 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
             wide = wide && by_eight(x[a], 2, xs, 2);
         }
         if (y[a]) {
-            if (!aligned(y[a], 2) || !span_of(y[a], 2, n, ys, d, 2, &out[a]) || !distinct(2, n, ys))
+            if (!aligned(y[a], 2) || !span_of(y[a], 2, n, ys, d, 2, &out[a]) || !distinct(2, n, ys, d))
                 return LF_ERR_INVALID_ARG;
             if (!small(ys)) return LF_ERR_UNSUPPORTED;
             p.yt[a] = static_cast<int>(ys[0]);
@@ -428,6 +446,8 @@ lf_status lf_attn_cache_append(const void* k, const void* v, const void* q, void
     for (const Span& a : in)
         for (const Span& b : out)
             if (a.meets(b)) return LF_ERR_INVALID_ARG;
+    const void* const written[7] = {k_cache, v_cache, k_par, v_par, k_held, v_held, q_out};
+    if (same_twice(written, 7)) return LF_ERR_INVALID_ARG;
     if (n_tokens == 0) return LF_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms = 0;
@@ -493,7 +513,7 @@ lf_status lf_attn_cache_fwd(const void* q, void* out, const int64_t* strides, co
     const Strides<2> by_q(n, strides), by_out(n, strides + 2);
     Span a, b;
     if (!span_of(q, 2, n, by_q.s, d, 2, &a) || !span_of(out, 2, n, by_out.s, d, 2, &b) ||
-        !distinct(2, n, by_out.s) || !by_eight(q, 2, by_q.s, 2) || !aligned(out, 2) || a.meets(b))
+        !distinct(2, n, by_out.s, d) || !by_eight(q, 2, by_q.s, 2) || !aligned(out, 2) || a.meets(b))
         return LF_ERR_INVALID_ARG;
     const uint64_t need = workspace_of(sh, d, bits);
     if (need > 0 && !workspace) return LF_ERR_INVALID_ARG;

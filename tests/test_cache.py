@@ -200,3 +200,19 @@ def test_sizes_past_32_bits_do_not_wrap():
                dict(n_tokens=2, q_heads=0)):
         with pytest.raises(ValueError, match="n_tokens|q_heads"):
             kv_cache.Plan(cache, i(2, 3), i(3), i(2), r=3, **kw)
+
+
+@pytest.mark.parametrize("what,kw", [
+    ("rotary", dict(ko=4 * FAKE)), ("rotary", dict(qo=6 * FAKE)),                     # two outputs in one place
+    ("rotary", dict(s=i64(*[8192, 4096, 64] * 5 + [8192, 4096, 63]))),                # rows that reach into the next
+    ("rotary", dict(s=i64(*[8192, 4096, 64] * 3 + [8192, 64, 64] + [8192, 4096, 64] * 2))),      # heads on tokens
+    ("rotary", dict(s=i64(*[8192, 4096, 64] * 4 + [4032, 4096, 64] + [8192, 4096, 64]))),         # samples on heads
+    ("append", dict(hk=7 * FAKE, hv=7 * FAKE)), ("append", dict(hk=4 * FAKE)), ("append", dict(vc=5 * FAKE)),
+    ("append", dict(hv=5 * FAKE)), ("append", dict(s=i64(*[256, 64] * 5 + [128, 64]))),
+    ("append", dict(bits=4, kp=8 * FAKE, vp=8 * FAKE)),
+    ("fwd", dict(s=i64(256, 64, 256, 32))), ("fwd", dict(s=i64(256, 64, 192, 64))), ("fwd", dict(s=i64(256, 64, 64, 64))),
+])
+def test_outputs_that_lie_on_one_another_are_refused(lib, what, kw):
+    fn, args, order = {"rotary": (lib.lf_attn_rotary, ROTARY, ROTARY_ORDER), "fwd": (lib.lf_attn_cache_fwd, FWD, FWD_ORDER),
+                       "append": (lib.lf_attn_cache_append, APPEND, APPEND_ORDER)}[what]
+    assert call(fn, args, order, **kw) == INVALID
