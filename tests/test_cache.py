@@ -190,6 +190,19 @@ def test_the_packing_is_one_to_one():
             assert torch.equal(ref.unpack(ref.pack(c, is_k), is_k), c)
 
 
+def test_strided_cache_tensors_are_refused():
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    u = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    h = lambda *s: torch.zeros(*s, dtype=torch.float16)  # noqa: E731
+    bad = z(2, 8, 2, 64).transpose(1, 2)
+    assert not bad.is_contiguous()
+    for args in ((bad, z(2, 2, 8, 64)), (z(2, 2, 8, 64), bad), (z(2, 2, 8, 128)[..., :64], z(2, 2, 8, 64)),
+                 (u(2, 2, 8, 32), u(2, 2, 8, 64)[..., ::2], h(2, 2, 8, 2, 2), h(2, 2, 8, 2, 2)),
+                 (u(2, 2, 8, 32), u(2, 2, 8, 32), h(2, 2, 8, 2, 2), h(2, 2, 2, 8, 2).transpose(2, 3))):
+        with pytest.raises(ValueError, match="contiguous"):
+            kv_cache.KVCache(*args)
+
+
 def test_sizes_past_32_bits_do_not_wrap():
     cache = kv_cache.KVCache(torch.zeros(4, 2, 8, 64).half(), torch.zeros(4, 2, 8, 64).half())
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731

@@ -122,6 +122,53 @@ def test_small_4_bit_queries_beside_a_large_one(d, hq, dtype):
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
 
 
+CUT = {  # dtype, bits, new, old, hq, hkv, d, page, r, dil, globals: units of single rows that several CTAs share
+    "12_on_1": (BF16, 16, [1], [3000], 12, 1, 64, 64, FULL, 1, None),
+    "16_on_1_d128": (F16, 16, [1], [2500], 16, 1, 128, 32, FULL, 1, [[0, 9]]),
+    "17_on_1": (F16, 16, [1], [2000], 17, 1, 64, 64, FULL, 1, None),
+    "34_on_2": (BF16, 16, [1, 1], [1500, 4000], 34, 2, 64, 16, FULL, 1, None),
+    "40_on_1_d128": (BF16, 16, [1], [2100], 40, 1, 128, 64, 2000, 1, [[0]]),
+    "128_on_1": (F16, 16, [1], [1600], 128, 1, 64, 256, FULL, 1, None),
+    "12_on_1_four_d128": (F16, 4, [1], [2500], 12, 1, 128, 32, FULL, 1, None),
+    "17_on_1_four": (BF16, 4, [1], [3000], 17, 1, 64, 64, FULL, 1, None),
+    "34_on_2_four": (F16, 4, [1, 1], [2600, 1500], 34, 2, 64, 32, FULL, 1, [[3, 0]] * 2),
+    "40_on_1_four_d128": (BF16, 4, [1], [3000], 40, 1, 128, 64, FULL, 1, None),
+    "dilated": (BF16, 16, [1, 1], [5000, 1200], 8, 4, 64, 64, 1000, [1, 2, 3, 7], [[0, 11, 4000]] * 2),
+    "dilated_20_on_2": (F16, 16, [1], [4500], 40, 2, 64, 32, 1200, [1, 3], [[1]]),
+    "dilated_four": (F16, 4, [1], [6000], 12, 3, 128, 64, 1500, [1, 2, 4], None),
+}
+
+
+@pytest.mark.parametrize("name", list(CUT))
+def test_units_of_many_heads_cut_between_ctas(name):
+    s = Step(540 + len(name), *CUT[name]).to_gpu()
+    past = s.globals_ is not None and bool((s.globals_ >= s.table.shape[1] * s.page).any())
+    assert s.plan.workspace_bytes > 0
+    s.plan.buffer.fill_(255)  # entries that the plan does not write: -1
+    s.plan.refresh()
+    cuts = s.plan.buffer[256 + 640 * 40:256 + 640 * 56].view(torch.int32).view(640, 4)  # (row, unit, last CTA, tile)
+    assert (cuts[:, 2] > 0).any()
+    got = kv_cache.fwd(s.cache, s.plan, s.q.cuda())
+    s.check(got)
+    assert torch.equal(got, kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
+    assert lf_attn.device_status() == ((5, 1) if past else (0, 0))
+
+
+def test_flags_of_rows_taken_together():
+    """A page outside the cache, then rows behind the table, in tiles: bit 2 and no other."""
+    s = Step(550, F16, 16, [280, 21], [40, 10], 4, 2, 64, 16, 25, globals_=[[0, 33], [1, 2]])
+    s.table[0, 2], s.table[1, 0] = -5, 1 << 20
+    s.to_gpu()
+    s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
+    assert lf_attn.device_status() == (5, 4)
+    s = Step(551, BF16, 16, [304], [40], 2, 2, 64, 16, 25)
+    s.context += 16  # the last 8 rows are behind the table
+    s.rows = [(0, 56 + i) if i < 296 else None for i in range(304)]
+    s.to_gpu()
+    s.check(kv_cache.fwd(s.cache, s.plan, s.q.cuda()))
+    assert lf_attn.device_status() == (5, 4)
+
+
 @pytest.mark.parametrize("cu", [[0, 430, 10, 530, 250], [0, 350, 260, 290, 120], [0, 700, 0, 700, 700]])
 def test_no_row_is_one_where_cu_tokens_decreases(cu):
     """Rows that two sequences could claim: none is taken, in tiles or single rows, by the cache or the attention; flagged."""
