@@ -117,16 +117,27 @@ class Plan:
             self.n_tokens, self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.d, self.bits,
             self.r)
         self.device_index = context.get_device()
-        self.buffer = _on_stream(stream, context.get_device(), self._inputs(),
-                                 lambda raw: torch.empty(size, dtype=torch.uint8, device=context.device))
+
+        def make(raw):
+            self._streams = {raw}
+            return torch.empty(size, dtype=torch.uint8, device=context.device)
+
+        self.buffer = _on_stream(stream, self.device_index, self._inputs(), make)
         self.refresh(stream)
 
     def _inputs(self):
         return self.cu_tokens, self.context, self.table, self.global_idx
 
+    def _used_by(self, raw):
+        """The buffer, which only the plan holds, outlives the plan until the work of every stream that read it is done."""
+        if raw not in self._streams and not torch.cuda.is_current_stream_capturing():
+            self.buffer.record_stream(torch.cuda.current_stream(self.device_index))
+            self._streams.add(raw)
+
     def refresh(self, stream: Optional[torch.cuda.Stream] = None) -> "Plan":
         """Lays the step out again, from what cu_tokens, context and global_idx hold when the call runs."""
         def call(raw):
+            self._used_by(raw)
             st = lf_attn.load().lf_attn_cache_plan(
                 _ptr(self.cu_tokens), _ptr(self.context), self.n_seqs, self.n_tokens, _ptr(self.global_idx),
                 self.n_global, self.page, self.max_pages, self.q_heads, self.kv_heads, self.d, self.bits,
@@ -207,6 +218,7 @@ def append(cache: KVCache, plan: Plan, k: torch.Tensor, v: torch.Tensor, q: Opti
         if held is True:
             hk, hv = new(k), new(v)
         if n > 0:  # empty tensors have no address
+            plan._used_by(raw)
             for t in (hk, hv, q_out):
                 strides.extend((0, 0) if t is None else t.stride()[:2])
             st = lf_attn.load().lf_attn_cache_append(
@@ -244,6 +256,7 @@ def fwd(cache: KVCache, plan: Plan, q: torch.Tensor, scale: Optional[float] = No
         y = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
         if n == 0:  # empty tensors have no address
             return y
+        plan._used_by(raw)
         ws = workspace
         if ws is None and plan.workspace_bytes:
             ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)

@@ -188,6 +188,28 @@ def test_no_row_is_one_where_cu_tokens_decreases(cu):
         s.check(kv_cache.fwd(s.cache, s.plan, q))
 
 
+@pytest.mark.parametrize("call", ["fwd", "append"])
+def test_a_plan_outlives_its_use_on_another_stream(call):
+    """A plan made on a side stream, used on the current one behind a wait, then dropped: its memory is not given out on the
+    side stream before that use."""
+    s = Step(580, BF16, 16, [1, 2], [300, 40], 4, 2, 64, 16, FULL).to_gpu()
+    q, k, v, side = s.q.cuda(), s.k.cuda(), s.v.cuda(), torch.cuda.Stream()
+    plan = kv_cache.Plan(s.cache, s.plan.table, s.plan.cu_tokens, s.plan.context, s.N, s.hq, s.r, stream=side)
+    torch.cuda.synchronize()
+    size = plan.buffer.numel()
+    torch.cuda._sleep(100_000_000)
+    got = kv_cache.fwd(s.cache, plan, q) if call == "fwd" else kv_cache.append(s.cache, plan, k, v, q=q)
+    del plan
+    with torch.cuda.stream(side):
+        taken = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert lf_attn.device_status() == (0, 0) and len(taken) == 4
+    if call == "fwd":
+        s.check(got)
+    else:
+        assert torch.equal(got, q)
+
+
 def test_windows_and_dilations_past_32_bits():
     s = Step(560, BF16, 16, [1], [300], 2, 2, 64, 16, FULL).to_gpu()
     q = s.q.cuda()
