@@ -219,8 +219,9 @@ lf_status lf_attn_merge_rows(const float* ml, const float* acc, int n_parts, int
  *   freqs       DEVICE double [rot / 2], radians per position
  *   in_dtype, out_dtype   the same, or LF_F32 to a 16-bit type
  *   Pointers are aligned to their element.  16-byte aligned rows with
- *   d % 16 == 0 and rot % 16 == 0 (8 when interleaved) move 16 values at a
- *   time; others go value by value.
+ *   d % 16 == 0, interleaved or with rot % 16 == 0, move 16 values at a time.
+ *   Others go by pairs, two at a time where rows are 16-byte aligned, d is
+ *   even, the pairs are in halves and rot % 4 == 0.
  */
 lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
                          const int64_t* strides, int B, int q_heads, int kv_heads, int T, int d, const int32_t* pos,
@@ -234,8 +235,10 @@ lf_status lf_attn_rotary(const void* q, const void* k, const void* v, void* q_ou
  *   N(p) = { p - dil[h] * t : 0 <= t <= r, p - dil[h] * t >= 0 }
  *          U { g in G : g <= p }                         for p not in G;
  *   N(p) = 0 .. p                                        for p in G,
- * each key once: the forward's key set with nothing behind the token, so the
- * last row of lf_attn_fwd over the same keys is the same row.  q_heads /
+ * each key once: the forward's key set with nothing behind the token.  The
+ * last row of lf_attn_fwd over the same keys is the same row; its other rows
+ * see r keys behind them too, so a model that was trained with lf_attn_fwd's
+ * two-sided window meets another mask here.  q_heads /
  * kv_heads query heads share a kv head.
  *
  * The cache has n_pages pages of `page` tokens (a power of two, 8..256);

@@ -16,9 +16,9 @@
 // of a group: its minimum and maximum are two shuffles, and each lane's codes
 // make one 32-bit word of a K row and one unit of a V row for each of two
 // lanes, exchanged so that both store whole words.  (Prompts of 4099 tokens,
-// 36 rows of 64, 16 bits: 9.7 us, 3.9 TB/s; 16384 tokens of 32 rows, 4 bits
-// and what they hold: 42 us, 3.7 TB/s, 20 of them for the codes, which
-// instructions bound.)
+// 36 rows of 64, 16 bits: 9.6 us, 3.9 TB/s, and 11.1 where nothing is in L2;
+// 16384 tokens of 32 rows, 4 bits and what they hold: 42 us, 3.4 TB/s, 20 of
+// them for the codes, which instructions bound.)
 #pragma once
 #include <type_traits>
 

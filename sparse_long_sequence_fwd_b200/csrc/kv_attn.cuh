@@ -73,6 +73,9 @@ __host__ __device__ constexpr int kv_block(int bits) { return kKvWarps * 16 * kv
 
 // Query rows of a tile, at most.  Over 4 bits of d = 128 16 rows spill (16
 // sequences of 6 drafts, 4000 keys, 32 heads on 8: 109 us against 88 with 8).
+// Of d = 64 they spill too (56 bytes a thread, 164 with f16 queries) but take
+// less on prompts: 4096 rows, 12 heads, window 256, 84 us against 105 with 8 (f16
+// 104 : 109); the drafts above 43.5 : 46.3 (f16 56.0 : 48.5).
 __host__ __device__ constexpr int kv_tile_rows(int d, int bits) { return d == 128 && bits == 4 ? 8 : 16; }
 
 // CTAs of four warps that an SM holds at once, by registers (128 to 255 a

@@ -19,7 +19,9 @@
 // Units stay whole where cutting them would gain less than the merge costs
 // (decided on the host from the window and the number of rows): a CTA takes
 // the units that begin in its range, and nothing is merged.  (A global row,
-// which sees every key, is then one CTA's work too.)
+// which sees every key, is then one CTA's work a head too: 16 single tokens at
+// 32768, 12 heads of 64, window 256, take 8 us, and 308 where one of them is
+// global.)
 //
 // Bound: latency (a few KB; 7 to 18 us for 1 to 64 sequences, 40 us for a
 // prompt of 16384 rows, once for all layers of a step).  The global lists take
@@ -37,8 +39,8 @@ constexpr int kKvMaxCtas = 640;
 constexpr int kKvMinKeys = 256;        // keys (and units' costs) per CTA below which fewer CTAs take part
 // Keys whose time a unit's beginning and end take.  Without it the CTAs that
 // have the short rows at a prompt's start end last: 4096 rows that see all
-// before them, 16 heads on 2 of 128, 870 us against 1873 (4 bits 730 : 1371; 512
-// keys: 901 and 752); 4 sequences of up to 65536 over 4 bits 76 : 83.
+// before them, 16 heads on 2 of 128, 863 us against 1514 (4 bits 766 : 1098; 512
+// keys: 897 and 791); 4 sequences of up to 65536 over 4 bits 79.3 : 83.5.
 constexpr int kUnitKeys = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 4096, kPlanRows = 1024;  // up to which cu_tokens and the prefix sum are searched in shared memory

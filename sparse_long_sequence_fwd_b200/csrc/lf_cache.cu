@@ -157,8 +157,8 @@ bool may_cut_tiles(int64_t rows, int tpt, int kv_heads, int64_t keys, int64_t gr
 
 // Rows of a tile: as many as the sequences have each, up to what a unit holds.
 // Times in us, tiles against single rows: 4096 rows of a prompt, 12 heads of 64,
-// window 256: 71 : 815 (4 bits 83 : 823); 16 sequences of 4 drafts, 4000 keys,
-// 32 heads on 8 of 128: 53 : 153 (4 bits 62 : 100).
+// window 256: 71 : 481 (4 bits 84 : 579); 16 sequences of 4 drafts, 4000 keys,
+// 32 heads on 8 of 128: 53 : 148 (4 bits 63 : 97).
 // No tiles where heads are dilated, whose neighbouring rows share no keys.  Not
 // two rows in a unit of 16 either, which costs what two units of 8 do (8
 // sequences of 3, 8000 keys, 16 heads on 2 of 128: 32 against 28).

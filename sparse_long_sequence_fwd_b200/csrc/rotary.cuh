@@ -37,8 +37,11 @@ constexpr int kRotMaxD = 256;
 constexpr int kRotMaxTile = 16;   // tokens per CTA
 
 // Heads whose 16 values a thread holds at once: 64 bytes of either type.  Few,
-// so that 72 registers do and an SM holds seven CTAs (4096 tokens of 36 rows
-// of 64, bf16: 8.3 us; six CTAs 9.2, eight, which spill, 11.2).
+// so that an SM holds seven CTAs of 72 registers, which spill 8 to 68 bytes a
+// thread.  Over sets of inputs larger than L2: 4096 tokens of 36 rows of 64,
+// bf16, 8.9 us (six CTAs, which spill none to 8 bytes, 9.8), fp32 gradients of
+// 8192 tokens 19.0 (22.4), 16383 tokens of 32 rows, f16, 29.0 (28.0); eight
+// spill up to 120 bytes and took 11.2 us where seven took 8.3.
 template <typename T>
 constexpr int kRotItems = 4 / int(sizeof(T));
 constexpr int kRotCtas = 7;
